@@ -1,0 +1,118 @@
+/*
+ * ssd_glr.h - C ABI of the gated linear recurrence for NVIDIA B200 (sm_100a):
+ * the elementwise counterpart of the SSD layer in ssd_fwd.h.  Where the SSD
+ * layer's decay is one scalar a head over a P x N state, here every channel
+ * has a state of one value, and its decay and its input are gated token by
+ * token.  Per sequence s, token t and channel c:
+ *
+ *     q_t = exp(A_log[c]) * sigmoid(r[t, c])          a_t = exp(-q_t)
+ *     h_t = a_t * h_{t-1} + sqrt(1 - a_t^2) * sigmoid(i[t, c]) * x[t, c]
+ *     y[t, c] = h_t
+ *
+ * with h_{-1} = initial_states[s, c] (zeros when NULL) and final_states[s, c] =
+ * the state after the sequence's last token (the initial state where it has
+ * none).  r and i are raw gate logits.  States and all arithmetic are float32;
+ * y is rounded once to the io dtype.  Gates below sigmoid(-42.9) = 2^-62 are
+ * taken as 2^-62, and q above 87 as 87 (a < 2^-125).
+ *
+ * Layouts:
+ *     x, r, i          (batch, seqlen, channels)   io dtype, x_stride (r_stride,
+ *                      i_stride) elements from one token to the next: the three
+ *                      may be column ranges of one projection's output
+ *     y, dy, dx, dr, di (batch, seqlen, channels)  contiguous
+ *     A_log, dA_log    (channels)                  float32
+ *     initial_states, final_states and their gradients
+ *                      (nseq, channels)            float32
+ *     cu_seqlens       (num_seqs + 1)              int32
+ *     chunk_states     (batch, ceil(seqlen / 64), channels)  float32: the state
+ *                      that the update of token 64 k starts from
+ * nseq and cu_seqlens are as in ssd_fwd.h.  Pointers are naturally aligned
+ * device pointers owned by the caller; 16-byte aligned rows run faster.
+ * Outputs must not overlap inputs.  Ownership, threading and errors are as in
+ * ssd_fwd.h: nothing is allocated, arguments are validated before anything is
+ * launched, calls are asynchronous on `stream`, and what the host cannot see
+ * is in the workspace's status word (ssd_get_status).  The workspace needs no
+ * initialisation, may be reused by the next call on the same stream, and must
+ * not be shared by calls that can overlap (two captured graphs replayed on two
+ * streams need one each).
+ * Results do not depend on scheduling: the same call gives the same bits.
+ */
+#ifndef SSD_GLR_H_
+#define SSD_GLR_H_
+
+#include "ssd_fwd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SSD_GLR_CHUNK 64        /* tokens between two rows of chunk_states */
+
+typedef struct ssd_glr_params {
+    int batch;                  /* >= 1 (1 when num_seqs > 0) */
+    int seqlen;                 /* >= 0, tokens per row (total tokens when num_seqs > 0) */
+    int channels;               /* >= 1 */
+    int num_seqs;               /* > 0 iff cu_seqlens != NULL, at most 2^20 */
+    ssd_dtype io_dtype;         /* x, r, i, y, dy */
+    ssd_dtype grad_dtype;       /* dx, dr, di: SSD_DTYPE_F32, or io_dtype */
+    int64_t x_stride;           /* elements between tokens, >= channels */
+    int64_t r_stride;
+    int64_t i_stride;
+} ssd_glr_params;
+
+/* Bytes of device workspace (0 on invalid parameters). */
+SSD_API size_t ssd_glr_fwd_workspace_size(const ssd_glr_params *p);
+
+/* Forward.  initial_states, cu_seqlens, final_states and chunk_states may be
+ * NULL (zero states, equal rows, not written). */
+SSD_API ssd_status ssd_glr_fwd(const ssd_glr_params *p,
+                   const void *x, const void *r, const void *i, const float *A_log,
+                   const float *initial_states, const int32_t *cu_seqlens,
+                   void *y, float *final_states, float *chunk_states,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* Backward: the gradients of a loss L given dy = dL/dy and dfinal_states =
+ * dL/dfinal_states (NULL = 0).  With g_t = dL/dh_t, m_t = sqrt(1 - a_t^2):
+ *
+ *     g_t  = dy_t + a_{t+1} g_{t+1},   g_last = dy_last + dfinal
+ *     dx_t = g_t m_t sigmoid(i_t),     di_t = g_t m_t x_t sigmoid(i_t) sigmoid(-i_t)
+ *     dq_t = (a_t^2 / m_t) g_t sigmoid(i_t) x_t - a_t g_t h_{t-1}
+ *     dr_t = dq_t q_t sigmoid(-r_t),   dA_log = sum_t dq_t q_t
+ *     dinitial_states = a_first g_first   (dfinal for an empty sequence)
+ *
+ * dx, dr and di are in grad_dtype; dA_log (summed over rows and tokens) and
+ * dinitial_states (NULL: not written) are float32.  chunk_states is what
+ * ssd_glr_fwd wrote for the same inputs; with NULL the pass recomputes it into
+ * the workspace first (with_chunk_states = 0 in the size query). */
+SSD_API size_t ssd_glr_bwd_workspace_size(const ssd_glr_params *p, int with_chunk_states);
+
+SSD_API ssd_status ssd_glr_bwd(const ssd_glr_params *p,
+                   const void *x, const void *r, const void *i, const float *A_log,
+                   const float *initial_states, const int32_t *cu_seqlens, const float *chunk_states,
+                   const void *dy, const float *dfinal_states,
+                   void *dx, void *dr, void *di, float *dA_log, float *dinitial_states,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+/* One token of every row (decoding): state (batch, channels) float32 is read
+ * and overwritten; x, r, i (batch, channels) with x_stride (r_stride, i_stride)
+ * elements between rows, y (batch, channels) contiguous.  A forward with
+ * final_states followed by steps from that state reproduces the forward over
+ * the concatenated tokens.  No workspace. */
+typedef struct ssd_glr_step_params {
+    int batch;                  /* rows >= 0 (0: nothing to do) */
+    int channels;               /* >= 1 */
+    ssd_dtype io_dtype;
+    int64_t x_stride;           /* elements between rows, >= channels */
+    int64_t r_stride;
+    int64_t i_stride;
+} ssd_glr_step_params;
+
+SSD_API ssd_status ssd_glr_step(const ssd_glr_step_params *p,
+                   const void *x, const void *r, const void *i, const float *A_log,
+                   float *state, void *y, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSD_GLR_H_ */

@@ -1,0 +1,78 @@
+/*
+ * ssd_norm.h - C ABI of the layer norm around the SSD layer for NVIDIA B200
+ * (sm_100a), forward and backward: the norm before the block (optionally of
+ * the residual stream plus the block's input) and, with a gate and one group a
+ * head, the norm of the block's output that ssd_fwd_gated_norm applies, here
+ * as an operator of its own with its gradient.  Per row and group of
+ * P = dim / ngroups channels:
+ *
+ *     u = x                                  plain
+ *     u = sum = round(x + residual)          residual (rounded to the io dtype, and kept)
+ *     u = x * silu(z)                        gate (z and residual exclude one another)
+ *     mean = sum(u) / P,  rstd = 1 / sqrt(sum((u - mean)^2) / P + eps)
+ *     y = (u - mean) * rstd * weight + bias
+ *
+ * Statistics and all arithmetic are float32 (the variance is taken about the
+ * mean, in a second pass over the registers); y is rounded once.
+ *
+ * Layouts: x and z (rows, dim) io dtype with x_stride (z_stride) elements from
+ * one row to the next; residual, sum, y, dy (rows, dim) io dtype and
+ * dresidual, dx, dz (rows, dim) grad dtype, contiguous; weight, bias, dweight,
+ * dbias (dim) float32; mean, rstd (rows, ngroups) float32.  Pointers are
+ * naturally aligned device pointers; 16-byte aligned rows run faster.  Outputs
+ * must not overlap inputs.  Ownership, threading and errors are as in
+ * ssd_fwd.h.  Results do not depend on scheduling: the same call on the same
+ * device gives the same bits.
+ */
+#ifndef SSD_NORM_H_
+#define SSD_NORM_H_
+
+#include "ssd_fwd.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SSD_LAYER_NORM_MAX_GROUP 16384  /* channels of one group */
+
+typedef struct ssd_layer_norm_params {
+    int64_t rows;               /* >= 0, below 2^31 */
+    int dim;                    /* channels of a row >= 1 */
+    int ngroups;                /* >= 1, dim % ngroups == 0 */
+    float eps;                  /* >= 0 */
+    ssd_dtype io_dtype;
+    ssd_dtype grad_dtype;       /* dx, dz, dresidual: SSD_DTYPE_F32, or io_dtype */
+    int64_t x_stride;           /* elements between rows, >= dim */
+    int64_t z_stride;           /* >= dim where z is given */
+} ssd_layer_norm_params;
+
+/* Forward.  residual and sum come together (NULL: plain); z, bias, mean and
+ * rstd may be NULL (no gate, 0, not written). */
+SSD_API ssd_status ssd_layer_norm_fwd(const ssd_layer_norm_params *p,
+                   const void *x, const void *residual, const void *z,
+                   const float *weight, const float *bias,
+                   void *y, void *sum, float *mean, float *rstd, void *stream);
+
+/* Backward, given dy = dL/dy, the x (with a residual: the sum) and z of the
+ * forward, and its mean and rstd.  With xhat = (u - mean) * rstd:
+ *
+ *     du = rstd * (w dy - mean(w dy) - xhat * mean(w dy xhat))
+ *     dweight = sum over rows of dy xhat,   dbias = sum over rows of dy
+ *     dx = du + dresidual            (plain, residual; dresidual NULL = 0)
+ *     dx = du silu(z),  dz = du x sigmoid(z) (1 + z sigmoid(-z))      (gate)
+ *
+ * With a residual dx is the gradient of the sum, so of x and of residual.
+ * dbias may be NULL (not written); dz comes with z, dresidual not with z. */
+SSD_API size_t ssd_layer_norm_bwd_workspace_size(const ssd_layer_norm_params *p);
+
+SSD_API ssd_status ssd_layer_norm_bwd(const ssd_layer_norm_params *p,
+                   const void *x, const void *z, const float *weight,
+                   const float *mean, const float *rstd, const void *dy, const void *dresidual,
+                   void *dx, void *dz, float *dweight, float *dbias,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
+#ifdef __cplusplus
+}
+#endif
+
+#endif /* SSD_NORM_H_ */

@@ -24,6 +24,8 @@ from typing import Optional
 __all__ = [
     "ssd_fwd", "ssd_bwd", "ssd_fwd_summary", "ssd_state_combine", "ssd_decode_step", "SsdParams", "SsdStepParams", "SsdInstrumentation", "make_instrumentation", "workspace_size",
     "launch_count", "resolved_path", "library", "library_path", "STATUS", "PATHS", "SsdError",
+    "ssd_glr_fwd", "ssd_glr_bwd", "ssd_glr_step", "GLR_CHUNK", "SsdGlrParams", "SsdGlrStepParams",
+    "ssd_layer_norm_fwd", "ssd_layer_norm_bwd", "SsdLayerNormParams",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -38,7 +40,11 @@ DTYPES = {"f32": 0, "bf16": 1}
 
 EXPORTED = ("ssd_fwd", "ssd_fwd_instrumented", "ssd_fwd_gated_norm", "ssd_bwd", "ssd_bwd_workspace_size", "ssd_fwd_summary",
             "ssd_fwd_summary_workspace_size", "ssd_state_combine", "ssd_decode_step", "ssd_fwd_workspace_size", "ssd_get_status", "ssd_fwd_launch_count",
-            "ssd_fwd_resolved_path", "ssd_status_string", "ssd_abi_version")
+            "ssd_fwd_resolved_path", "ssd_status_string", "ssd_abi_version",
+            "ssd_glr_fwd", "ssd_glr_fwd_workspace_size", "ssd_glr_bwd", "ssd_glr_bwd_workspace_size", "ssd_glr_step",
+            "ssd_layer_norm_fwd", "ssd_layer_norm_bwd", "ssd_layer_norm_bwd_workspace_size")
+
+GLR_CHUNK = 64      # SSD_GLR_CHUNK: tokens between two rows of chunk_states
 
 
 class SsdError(RuntimeError):
@@ -70,6 +76,29 @@ class SsdStepParams(ctypes.Structure):
         ("batch", ctypes.c_int), ("nheads", ctypes.c_int), ("headdim", ctypes.c_int),
         ("dstate", ctypes.c_int), ("ngroups", ctypes.c_int), ("io_dtype", ctypes.c_int),
         ("dt_softplus", ctypes.c_int),
+    ]
+
+
+class SsdGlrParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("seqlen", ctypes.c_int), ("channels", ctypes.c_int), ("num_seqs", ctypes.c_int),
+        ("io_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64), ("i_stride", ctypes.c_int64),
+    ]
+
+
+class SsdGlrStepParams(ctypes.Structure):
+    _fields_ = [
+        ("batch", ctypes.c_int), ("channels", ctypes.c_int), ("io_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_int64), ("r_stride", ctypes.c_int64), ("i_stride", ctypes.c_int64),
+    ]
+
+
+class SsdLayerNormParams(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64), ("dim", ctypes.c_int), ("ngroups", ctypes.c_int), ("eps", ctypes.c_float),
+        ("io_dtype", ctypes.c_int), ("grad_dtype", ctypes.c_int),
+        ("x_stride", ctypes.c_int64), ("z_stride", ctypes.c_int64),
     ]
 
 
@@ -118,6 +147,23 @@ def library():
             lib.ssd_status_string.argtypes = [i32]
             lib.ssd_abi_version.restype = i32
             lib.ssd_abi_version.argtypes = []
+            gp, np_ = ctypes.POINTER(SsdGlrParams), ctypes.POINTER(SsdLayerNormParams)
+            lib.ssd_glr_fwd_workspace_size.restype = sz
+            lib.ssd_glr_fwd_workspace_size.argtypes = [gp]
+            lib.ssd_glr_fwd.restype = i32
+            lib.ssd_glr_fwd.argtypes = [gp] + [vp] * 9 + [vp, sz, vp]
+            lib.ssd_glr_bwd_workspace_size.restype = sz
+            lib.ssd_glr_bwd_workspace_size.argtypes = [gp, i32]
+            lib.ssd_glr_bwd.restype = i32
+            lib.ssd_glr_bwd.argtypes = [gp] + [vp] * 14 + [vp, sz, vp]
+            lib.ssd_glr_step.restype = i32
+            lib.ssd_glr_step.argtypes = [ctypes.POINTER(SsdGlrStepParams)] + [vp] * 7
+            lib.ssd_layer_norm_fwd.restype = i32
+            lib.ssd_layer_norm_fwd.argtypes = [np_] + [vp] * 10
+            lib.ssd_layer_norm_bwd_workspace_size.restype = sz
+            lib.ssd_layer_norm_bwd_workspace_size.argtypes = [np_]
+            lib.ssd_layer_norm_bwd.restype = i32
+            lib.ssd_layer_norm_bwd.argtypes = [np_] + [vp] * 11 + [vp, sz, vp]
             _lib = lib
     return _lib
 
@@ -502,3 +548,348 @@ def ssd_decode_step(x, dt, A_log, B, C, D, state, y=None, dt_softplus: bool = Tr
     if rc != 0:
         raise SsdError(rc, "ssd_decode_step")
     return y
+
+
+# ------------------------------------------------- gated linear recurrence, layer norm
+
+def _row_stride(name, t, dev, dtype, shape):
+    """`t` must be a `dtype` tensor of `shape` on `dev` whose rows (the last
+    dimension) are contiguous and lie one stride apart, as a column range of a
+    contiguous tensor does; returns that stride in elements."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
+    width = shape[-1]
+    if t.is_contiguous():
+        return width
+    stride, rows = None, 1
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    for size, step in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if stride is None:
+            stride = step
+        elif step != stride * rows:
+            raise ValueError(f"{name}'s rows must lie one stride apart, got strides {t.stride()}")
+        rows *= size
+    stride = width if stride is None else stride
+    if stride < width:
+        raise ValueError(f"{name}'s rows must not overlap, got strides {t.stride()}")
+    return stride
+
+
+def _grad_dtype(io, grad_dtype):
+    import torch
+    if grad_dtype is None:
+        return torch.float32
+    if grad_dtype not in (torch.float32, io):
+        raise ValueError(f"grad_dtype must be float32 or x's dtype {io}, got {grad_dtype}")
+    return grad_dtype
+
+
+def _dtype_code(dtype) -> int:
+    import torch
+    return 1 if dtype == torch.bfloat16 else 0
+
+
+class _on_device:
+    """Makes `dev` the current device for a call, where it is not."""
+
+    def __init__(self, dev):
+        import torch
+        index = dev.index
+        self._guard = None
+        if index is not None and index != torch.cuda.current_device():
+            self._guard = torch.cuda.device(dev)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+def _workspace(workspace, need, what, dev):
+    import torch
+    if need == 0:
+        raise SsdError(-2, what)
+    if workspace is None or workspace.numel() * workspace.element_size() < need:
+        return torch.empty(need, dtype=torch.uint8, device=dev)
+    return workspace
+
+
+def _validate_glr(x, r, i, A_log, initial_states=None, cu_seqlens=None, y=None, final_states=None,
+                  chunk_states=None, workspace=None, dy=None, dfinal_states=None):
+    """Every tensor argument of ssd_glr_fwd and ssd_glr_bwd (metadata only);
+    returns (nseq, strides of x, r and i)."""
+    import torch
+    io = _io_dtype(x)
+    if x.dim() != 3:
+        raise ValueError(f"x must be (batch, seqlen, channels), got {tuple(x.shape)}")
+    dev, shape = x.device, x.shape
+    b, T, D = shape
+    strides = tuple(_row_stride(n, t, dev, io, shape) for n, t in (("x", x), ("r", r), ("i", i)))
+    _check("A_log", A_log, dev, torch.float32, (D,), required=True)
+    nseq = b
+    if cu_seqlens is not None:
+        _check("cu_seqlens", cu_seqlens, dev, torch.int32)
+        if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+            raise ValueError("cu_seqlens must be 1-D with nseq + 1 >= 2 entries")
+        if b != 1:
+            raise ValueError("a packed batch (cu_seqlens) has batch 1")
+        nseq = cu_seqlens.numel() - 1
+    _check("initial_states", initial_states, dev, torch.float32, (nseq, D))
+    _check("y", y, dev, io, shape)
+    _check("final_states", final_states, dev, torch.float32, (nseq, D))
+    _check("chunk_states", chunk_states, dev, torch.float32, (b, -(-T // GLR_CHUNK), D))
+    _check("dy", dy, dev, io, shape)
+    _check("dfinal_states", dfinal_states, dev, torch.float32, (nseq, D))
+    _check_workspace(workspace, dev)
+    return nseq, strides
+
+
+def _glr_params(x, nseq, cu_seqlens, gdt, strides) -> SsdGlrParams:
+    b, T, D = x.shape
+    return SsdGlrParams(b, T, D, 0 if cu_seqlens is None else nseq, _dtype_code(x.dtype), _dtype_code(gdt), *strides)
+
+
+def ssd_glr_fwd(x, r, i, A_log, initial_states=None, cu_seqlens=None, return_final_states: bool = False,
+                return_chunk_states: bool = False, y=None, final_states=None, chunk_states=None, workspace=None,
+                stream=None, check_status: bool = False):
+    """Gated linear recurrence on the GPU through the C ABI: per channel
+    h_t = a_t h_{t-1} + sqrt(1 - a_t^2) sigmoid(i_t) x_t, a_t = exp(-exp(A_log) sigmoid(r_t)).
+
+    Returns y, or (y[, final_states][, chunk_states]) for those that are asked
+    for or given. x, r, i (batch, seqlen, channels) share the io dtype
+    (bfloat16 or float32) and may be column ranges of one tensor; A_log
+    (channels,), initial_states and final_states (nseq, channels) are float32;
+    cu_seqlens (nseq + 1,) int32 marks a packed batch (batch == 1).
+    chunk_states (batch, ceil(seqlen / GLR_CHUNK), channels) float32, the states
+    before every GLR_CHUNK-th token, is what ssd_glr_bwd can start from.
+    """
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_glr_fwd runs on CUDA tensors only")
+    lib = library()
+    nseq, strides = _validate_glr(x, r, i, A_log, initial_states, cu_seqlens, y, final_states, chunk_states, workspace)
+    p = _glr_params(x, nseq, cu_seqlens, torch.float32, strides)
+    b, T, D = x.shape
+    ref = ctypes.byref(p)
+    with _on_device(dev):
+        workspace = _workspace(workspace, lib.ssd_glr_fwd_workspace_size(ref), "ssd_glr_fwd_workspace_size", dev)
+        if y is None:
+            y = torch.empty((b, T, D), dtype=x.dtype, device=dev)
+        if return_final_states and final_states is None:
+            final_states = torch.empty((nseq, D), dtype=torch.float32, device=dev)
+        if return_chunk_states and chunk_states is None:
+            chunk_states = torch.empty((b, -(-T // GLR_CHUNK), D), dtype=torch.float32, device=dev)
+        st = _stream_handle(stream)
+        rc = lib.ssd_glr_fwd(ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states), _ptr(cu_seqlens),
+                             _ptr(y), _ptr(final_states), _ptr(chunk_states), _ptr(workspace),
+                             workspace.numel() * workspace.element_size(), st)
+        if rc != 0:
+            raise SsdError(rc, "ssd_glr_fwd")
+        if check_status:
+            rc = lib.ssd_get_status(_ptr(workspace), st)
+            if rc != 0:
+                raise SsdError(rc, "ssd_glr_fwd (device status)")
+    out = (y,) + tuple(t for t in (final_states, chunk_states) if t is not None)
+    return out if len(out) > 1 else y
+
+
+def ssd_glr_bwd(x, r, i, A_log, dy, initial_states=None, cu_seqlens=None, dfinal_states=None, chunk_states=None,
+                grad_dtype=None, want_dinitial: bool = True, workspace=None, stream=None,
+                check_status: bool = False) -> dict:
+    """Gradients of L given dy = dL/dy (and dL/dfinal_states) of ssd_glr_fwd
+    through the C ABI: dx, dr, di (with respect to the raw gates) in
+    `grad_dtype` (float32 unless x's dtype is asked for), dA_log and
+    dinitial_states (None without `want_dinitial`) in float32, each shaped like
+    its input and contiguous. `chunk_states` from the forward saves the pass
+    that recomputes them."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_glr_bwd runs on CUDA tensors only")
+    lib = library()
+    if dy is None:
+        raise ValueError("dy is required")
+    nseq, strides = _validate_glr(x, r, i, A_log, initial_states, cu_seqlens, None, None, chunk_states, workspace, dy,
+                                  dfinal_states)
+    gdt = _grad_dtype(x.dtype, grad_dtype)
+    p = _glr_params(x, nseq, cu_seqlens, gdt, strides)
+    shape, D = tuple(x.shape), x.shape[2]
+    ref = ctypes.byref(p)
+    with _on_device(dev):
+        need = lib.ssd_glr_bwd_workspace_size(ref, int(chunk_states is not None))
+        workspace = _workspace(workspace, need, "ssd_glr_bwd_workspace_size", dev)
+        dx, dr, di = (torch.empty(shape, dtype=gdt, device=dev) for _ in range(3))
+        dA_log = torch.empty(D, dtype=torch.float32, device=dev)
+        dinit = torch.empty((nseq, D), dtype=torch.float32, device=dev) if want_dinitial else None
+        st = _stream_handle(stream)
+        rc = lib.ssd_glr_bwd(ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states), _ptr(cu_seqlens),
+                             _ptr(chunk_states), _ptr(dy), _ptr(dfinal_states), _ptr(dx), _ptr(dr), _ptr(di),
+                             _ptr(dA_log), _ptr(dinit), _ptr(workspace),
+                             workspace.numel() * workspace.element_size(), st)
+        if rc != 0:
+            raise SsdError(rc, "ssd_glr_bwd")
+        if check_status:
+            rc = lib.ssd_get_status(_ptr(workspace), st)
+            if rc != 0:
+                raise SsdError(rc, "ssd_glr_bwd (device status)")
+    return {"dx": dx, "dr": dr, "di": di, "dA_log": dA_log, "dinitial_states": dinit}
+
+
+def _validate_glr_step(x, r, i, A_log, state, y=None):
+    """Every tensor argument of ssd_glr_step; returns the strides of x, r and i."""
+    import torch
+    io = _io_dtype(x)
+    if x.dim() != 2:
+        raise ValueError(f"x must be (batch, channels), got {tuple(x.shape)}")
+    dev, shape = x.device, x.shape
+    strides = (_row_stride("x", x, dev, io, shape), _row_stride("r", r, dev, io, shape),
+               _row_stride("i", i, dev, io, shape))
+    _check("A_log", A_log, dev, torch.float32, (shape[1],), required=True)
+    _check("state", state, dev, torch.float32, shape, required=True)
+    _check("y", y, dev, io, shape)
+    return strides
+
+
+def ssd_glr_step(x, r, i, A_log, state, y=None, stream=None):
+    """One decoding step of the gated linear recurrence for every row through
+    the C ABI; updates `state` (batch, channels) float32 in place and returns y.
+    x, r, i (batch, channels) share the io dtype and may be column ranges of
+    one tensor; A_log (channels,) is float32."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_glr_step runs on CUDA tensors only")
+    lib = library()
+    strides = _validate_glr_step(x, r, i, A_log, state, y)
+    b, D = x.shape
+    p = SsdGlrStepParams(b, D, _dtype_code(x.dtype), *strides)
+    with _on_device(dev):
+        if y is None:
+            y = torch.empty((b, D), dtype=x.dtype, device=dev)
+        rc = lib.ssd_glr_step(ctypes.byref(p), _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(state), _ptr(y),
+                              _stream_handle(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_glr_step")
+    return y
+
+
+def _validate_layer_norm(x, weight, bias=None, residual=None, z=None, ngroups=1, y=None):
+    """Every tensor argument of ssd_layer_norm_fwd; returns (rows, dim, stride
+    of x, stride of z)."""
+    import torch
+    io = _io_dtype(x)
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"x must be (..., dim) with dim >= 1, got {tuple(x.shape)}")
+    dev, shape = x.device, x.shape
+    D = shape[-1]
+    if ngroups < 1 or D % ngroups:
+        raise ValueError(f"ngroups must divide dim {D}, got {ngroups}")
+    if residual is not None and z is not None:
+        raise ValueError("residual and z exclude one another")
+    xs = _row_stride("x", x, dev, io, shape)
+    zs = D if z is None else _row_stride("z", z, dev, io, shape)
+    _check("residual", residual, dev, io, shape)
+    _check("weight", weight, dev, torch.float32, (D,), required=True)
+    _check("bias", bias, dev, torch.float32, (D,))
+    _check("y", y, dev, io, shape)
+    return x.numel() // D, D, xs, zs
+
+
+def ssd_layer_norm_fwd(x, weight, bias=None, residual=None, z=None, ngroups: int = 1, eps: float = 1e-5,
+                       return_stats: bool = False, y=None, stream=None):
+    """Layer norm on the GPU through the C ABI, over the last dimension or each
+    of its `ngroups` groups: y = (u - mean) rstd weight + bias with u = x, u =
+    x + residual (rounded to x's dtype and returned) or u = x * silu(z).
+
+    Returns y, or (y[, sum][, mean, rstd]): sum where `residual` is given, the
+    statistics (rows..., ngroups) float32 with `return_stats`. x, residual and z
+    (..., dim) share the io dtype (bfloat16 or float32); x and z may be column
+    ranges of a wider tensor. weight and bias (dim,) are float32. With z and one
+    group a head this is the output norm that ssd_fwd applies given z and
+    norm_weight."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_layer_norm_fwd runs on CUDA tensors only")
+    lib = library()
+    rows, D, xs, zs = _validate_layer_norm(x, weight, bias, residual, z, ngroups, y)
+    code = _dtype_code(x.dtype)
+    p = SsdLayerNormParams(rows, D, ngroups, eps, code, code, xs, zs)
+    shape = tuple(x.shape)
+    with _on_device(dev):
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=dev)
+        total = None if residual is None else torch.empty(shape, dtype=x.dtype, device=dev)
+        mean = rstd = None
+        if return_stats:
+            mean = torch.empty(shape[:-1] + (ngroups,), dtype=torch.float32, device=dev)
+            rstd = torch.empty(shape[:-1] + (ngroups,), dtype=torch.float32, device=dev)
+        rc = lib.ssd_layer_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(z), _ptr(weight), _ptr(bias),
+                                    _ptr(y), _ptr(total), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_layer_norm_fwd")
+    out = (y,) + tuple(t for t in (total, mean, rstd) if t is not None)
+    return out if len(out) > 1 else y
+
+
+def _validate_layer_norm_bwd(x, weight, dy, mean, rstd, z=None, dresidual=None, ngroups=1, grad_dtype=None,
+                             workspace=None):
+    """Every tensor argument of ssd_layer_norm_bwd; returns (rows, dim, stride
+    of x, stride of z, the gradients' dtype)."""
+    import torch
+    rows, D, xs, zs = _validate_layer_norm(x, weight, None, None, z, ngroups)
+    gdt = _grad_dtype(x.dtype, grad_dtype)
+    dev, shape = x.device, tuple(x.shape)
+    if dresidual is not None and z is not None:
+        raise ValueError("dresidual and z exclude one another")
+    _check("dy", dy, dev, x.dtype, shape, required=True)
+    _check("mean", mean, dev, torch.float32, shape[:-1] + (ngroups,), required=True)
+    _check("rstd", rstd, dev, torch.float32, shape[:-1] + (ngroups,), required=True)
+    _check("dresidual", dresidual, dev, gdt, shape)
+    _check_workspace(workspace, dev)
+    return rows, D, xs, zs, gdt
+
+
+def ssd_layer_norm_bwd(x, weight, dy, mean, rstd, z=None, dresidual=None, ngroups: int = 1, grad_dtype=None,
+                       workspace=None, stream=None) -> dict:
+    """Gradients of L given dy = dL/dy of ssd_layer_norm_fwd through the C ABI:
+    dx and dz (None without z) in `grad_dtype` (float32 unless x's dtype is
+    asked for), dweight and dbias float32. mean and rstd are the forward's. For
+    a forward with a residual pass its sum as x; `dresidual` (in the gradients'
+    dtype) is then the gradient that arrives at the sum by the residual stream,
+    and dx the gradient of x and of residual."""
+    import torch
+    dev = x.device
+    if dev.type != "cuda":
+        raise ValueError("ssd_layer_norm_bwd runs on CUDA tensors only")
+    lib = library()
+    rows, D, xs, zs, gdt = _validate_layer_norm_bwd(x, weight, dy, mean, rstd, z, dresidual, ngroups, grad_dtype,
+                                                    workspace)
+    p = SsdLayerNormParams(rows, D, ngroups, 0.0, _dtype_code(x.dtype), _dtype_code(gdt), xs, zs)
+    ref, shape = ctypes.byref(p), tuple(x.shape)
+    with _on_device(dev):
+        workspace = _workspace(workspace, lib.ssd_layer_norm_bwd_workspace_size(ref),
+                               "ssd_layer_norm_bwd_workspace_size", dev)
+        dx = torch.empty(shape, dtype=gdt, device=dev)
+        dz = None if z is None else torch.empty(shape, dtype=gdt, device=dev)
+        dw = torch.empty(D, dtype=torch.float32, device=dev)
+        db = torch.empty(D, dtype=torch.float32, device=dev)
+        rc = lib.ssd_layer_norm_bwd(ref, _ptr(x), _ptr(z), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
+                                    _ptr(dresidual), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(workspace),
+                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    if rc != 0:
+        raise SsdError(rc, "ssd_layer_norm_bwd")
+    return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
