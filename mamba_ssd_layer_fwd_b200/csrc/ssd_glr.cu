@@ -1,106 +1,535 @@
 // Gated linear recurrence (include/ssd_glr.h): a state of one value a channel,
 //     q = exp(A_log) sigmoid(r),  a = exp(-q),  h <- a h + sqrt(1 - a^2) sigmoid(i) x,
-// forward, backward and single-token step.  One thread walks one channel of
-// one sequence.
+// forward, backward and single-token step.
+//
+// Every token maps the state h -> a h + b, and maps compose:
+// (A2, B2) o (A, B) = (A A2, A2 B + B2).  A row is cut into tiles of tokens and
+// each tile into runs of L tokens, one run a warp, with V adjacent channels a
+// lane.  A thread reads its run once, keeps (a, b) in registers and composes
+// them; the runs' maps meet in shared memory, the tiles' maps through L2, and
+// the thread replays its run from the state that enters it.  So x, r, i are
+// read once and y written once, however long the row: the floor is HBM.
+//
+// Tiles of one row wait for earlier tiles' maps.  Work is handed out by a
+// ticket, earlier tiles first, and a tile publishes its own map before it
+// waits, so a wait only ever concerns CTAs that already run.  The state
+// entering tile k is built from the state after the last whole group of
+// kGroup tiles, published by that group's last tile, and the maps of the tiles
+// since, always in the same order: results do not depend on timing, and the
+// chain of dependent waits is ntiles / kGroup long.
+#include <initializer_list>
+#include <type_traits>
+
 #include "ssd_glr.cuh"
 #include "ssd_glr.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kGroup = 16;          // tiles between two published states
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-glr_fwd_kernel(GlrArgs g, T *__restrict__ y, float *__restrict__ final_states, float *__restrict__ chunk_states)
+// Work split of one call (host and device).
+struct Tiling {
+    int ntiles, nblk, rows;         // tiles of a row, channel blocks, rows
+    int *ticket, *done;             // work counter; per channel block: finished CTAs (backward)
+    int *map_flag, *state_flag;     // [item], [row][group][blk]
+    float2 *maps;                   // [row][tile][D]
+    float *states;                  // [row][group][D]
+};
+
+// The row's position of the CTA's tile, counted along the direction of the scan.
+struct Item {
+    int row, step, blk;
+};
+
+__device__ __forceinline__ Item item_of(const Tiling &w, int ticket)
 {
-    const int c = blockIdx.y * kThreads + threadIdx.x, s = blockIdx.x;
-    const SeqSpan span = seq_span(g, s, blockIdx.y == 0 && threadIdx.x == 0);
-    if (c >= g.D) return;
-    const float rate = expf(g.A_log[c]);
-    float h = g.init ? g.init[(size_t)s * g.D + c] : 0.0f;
-    for (long long t = span.lo; t < span.hi; ++t) {
-        const long long in_row = g.cu ? t : t - span.lo;
-        if (chunk_states && in_row % SSD_GLR_CHUNK == 0)
-            chunk_states[((g.cu ? 0 : (long long)s * g.nchunk) + in_row / SSD_GLR_CHUNK) * g.D + c] = h;
-        const Gate k = gate(to_f32(static_cast<const T *>(g.r)[t * g.rs + c]),
-                            to_f32(static_cast<const T *>(g.i)[t * g.is + c]), rate);
-        h = fmaf(k.a, h, k.m * k.si * to_f32(static_cast<const T *>(g.x)[t * g.xs + c]));
-        if (y) y[t * g.D + c] = from_f32<T>(h);
-    }
-    if (final_states) final_states[(size_t)s * g.D + c] = h;
+    const int per = w.rows * w.nblk;
+    Item it;
+    it.step = ticket / per;
+    const int rem = ticket - it.step * per;
+    it.row = rem / w.nblk;
+    it.blk = rem - it.row * w.nblk;
+    return it;
 }
 
-template <typename T, typename G>
-__global__ void __launch_bounds__(kThreads)
-glr_bwd_kernel(GlrArgs g, const float *__restrict__ chunk_states, const T *__restrict__ dy,
+// Marks of a packed batch's tile: for each token the sequence that starts
+// (ends) with it, or -1.
+template <int TOKENS>
+struct Marks {
+    int first[TOKENS], last[TOKENS];
+};
+
+// Fills the marks of tokens [t0, t0 + TOKENS), gives sequences without tokens
+// that lie in the tile to `empty`, and checks this CTA's share of cu_seqlens.
+template <int TOKENS, typename Empty>
+__device__ __forceinline__ void mark_sequences(const GlrArgs &g, Marks<TOKENS> &m, int t0, long long cta, long long nctas,
+                                               bool lead, Empty empty)
+{
+    const int tid = threadIdx.x, n = blockDim.x;
+    for (int k = tid; k < TOKENS; k += n) m.first[k] = m.last[k] = -1;
+    __syncthreads();
+    // first sequence that may reach into the tile (the array is short, or searched by halves)
+    int lo = 0;
+    if (g.nseq > 1024) {
+        int hi = g.nseq;                                  // smallest s with cu[s + 1] >= t0
+        while (lo < hi) {
+            const int mid = (lo + hi) >> 1;
+            if (g.cu[mid + 1] >= t0) hi = mid; else lo = mid + 1;
+        }
+    }
+    for (int s = lo + tid; s < g.nseq; s += n) {
+        const int a = g.cu[s], b = g.cu[s + 1];
+        if (a > t0 + TOKENS) break;
+        if (b > a) {
+            if (a >= t0 && a < t0 + TOKENS) m.first[a - t0] = s;
+            if (b > t0 && b <= t0 + TOKENS) m.last[b - 1 - t0] = s;
+        } else if (lead && a >= t0 && (a < t0 + TOKENS || a == g.T)) {
+            // at the end of the row: only the last tile may take it
+            if (a < t0 + TOKENS || t0 + TOKENS >= g.T) empty(s);
+        }
+    }
+    const long long per = (g.nseq + nctas - 1) / nctas;
+    const long long end = min((cta + 1) * per, (long long)g.nseq);
+    for (long long s = cta * per + tid; s < end; s += n) {
+        const int a = g.cu[s], b = g.cu[s + 1];
+        if (a > b || (s == 0 && a != 0) || (s == g.nseq - 1 && b != g.T)) set_status(g.status, kDevBadSeqlens);
+    }
+    __syncthreads();
+}
+
+// Shared memory of one scan over a CTA's tile: C = 32 V channels, W warps.
+template <int V, int W>
+struct ScanSmem {
+    float2 run[W][32 * V];          // map of each warp's run
+    float2 tile[kGroup / 2][32 * V];  // maps of the group's earlier tiles, by pairs
+    float state[32 * V];            // state after the group before
+};
+
+// The exchange between the tiles of a row.  run[] holds the runs' maps in scan
+// order; publishes the tile's map (and, for a group's last tile, the state
+// after it) and returns in h the state entering run `w`.  `start` is the state
+// entering the row.
+template <int V, int W, bool PACKED>
+__device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, int D, int c, bool live, int w, int lane,
+                                            const float (&start)[V], ScanSmem<V, W> &sm, int *status, float (&h)[V])
+{
+    const int in_group = it.step % kGroup, group = it.step / kGroup;
+    const long long row_tile = (long long)it.row * tl.ntiles;
+    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup;
+    if (tl.ntiles > 1) {
+        if (w == 0) {
+            if (it.step + 1 < tl.ntiles) {
+                float A[V], B[V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+                for (int k = 0; k < W; ++k)
+#pragma unroll
+                    for (int v = 0; v < V; ++v) {
+                        const float2 m = sm.run[k][lane * V + v];
+                        compose_map<PACKED>(A[v], B[v], m.x, m.y);
+                    }
+                if (live) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v)
+                        __stcg(&tl.maps[(row_tile + it.step) * D + c + v], make_float2(A[v], B[v]));
+                }
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) st_release(&tl.map_flag[(row_tile + it.step) * tl.nblk + it.blk], 1);
+            }
+        }
+        // pairs of the group's earlier tiles, spread over the warps
+        for (int pair = w; pair * 2 < in_group; pair += W) {
+            float A[V], B[V];
+#pragma unroll
+            for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+            const int t0 = group * kGroup + pair * 2, cnt = min(2, in_group - pair * 2);
+            bool ok = wait_flag(&tl.map_flag[(row_tile + t0) * tl.nblk + it.blk], status);
+            if (ok && cnt > 1) ok = wait_flag(&tl.map_flag[(row_tile + t0 + 1) * tl.nblk + it.blk], status);
+            if (ok && live) {
+                float2 m[2][V];
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    m[0][v] = __ldcg(&tl.maps[(row_tile + t0) * D + c + v]);
+                    m[1][v] = cnt > 1 ? __ldcg(&tl.maps[(row_tile + t0 + 1) * D + c + v]) : make_float2(1.0f, 0.0f);
+                }
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    A[v] = m[0][v].x, B[v] = m[0][v].y;
+                    compose_map<PACKED>(A[v], B[v], m[1][v].x, m[1][v].y);
+                }
+            }
+#pragma unroll
+            for (int v = 0; v < V; ++v) sm.tile[pair][lane * V + v] = make_float2(A[v], B[v]);
+        }
+        if (w == W - 1 && group > 0) {
+            const long long at = (long long)it.row * ngroups + group - 1;
+            const bool ok = wait_flag(&tl.state_flag[at * tl.nblk + it.blk], status);
+#pragma unroll
+            for (int v = 0; v < V; ++v) sm.state[lane * V + v] = ok && live ? __ldcg(&tl.states[at * D + c + v]) : 0.0f;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) h[v] = group > 0 ? sm.state[lane * V + v] : start[v];
+    for (int pair = 0; pair * 2 < in_group; ++pair)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 m = sm.tile[pair][lane * V + v];
+            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
+        }
+    for (int k = 0; k < w; ++k)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 m = sm.run[k][lane * V + v];
+            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
+        }
+    if (w == W - 1 && in_group == kGroup - 1 && it.step + 1 < tl.ntiles &&
+        *reinterpret_cast<volatile int *>(status) != kDevTimeout) {
+        const long long at = (long long)it.row * ngroups + group;
+        if (live) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const float2 m = sm.run[W - 1][lane * V + v];
+                __stcg(&tl.states[at * D + c + v], apply_map<PACKED>(m.x, m.y, h[v]));
+            }
+        }
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release(&tl.state_flag[at * tl.nblk + it.blk], 1);
+    }
+}
+
+__device__ __forceinline__ int take_ticket(const Tiling &tl, int *slot)
+{
+    if (tl.ntiles == 1) return blockIdx.x;
+    if (threadIdx.x == 0) *slot = atomicAdd(tl.ticket, 1);
+    __syncthreads();
+    return *slot;
+}
+
+// y (NULL: chunk states only), final_states and chunk_states may be NULL
+template <typename T, int V, int L, int W, bool PACKED>
+__global__ void __launch_bounds__(32 * W, 512 / (32 * W))
+glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ final_states,
+               float *__restrict__ chunk_states)
+{
+    __shared__ ScanSmem<V, W> sm;
+    __shared__ Marks<PACKED ? L * W : 1> marks;
+    __shared__ int slot;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const Item it = item_of(tl, take_ticket(tl, &slot));
+    const int c = (it.blk * 32 + lane) * V;
+    const bool live = c < g.D;
+    const int tile0 = it.step * (L * W), t0 = tile0 + w * L;       // token in the row
+    const long long row0 = (long long)it.row * g.T;                // token of the row's start on the flat axis
+
+    Vec<T, V> xr[L], rr[L], ir[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        if (live && t0 + j < g.T) {
+            const long long t = row0 + t0 + j;
+            rr[j] = load_stream<T, V>(static_cast<const T *>(g.r) + t * g.rs + c);
+            ir[j] = load_stream<T, V>(static_cast<const T *>(g.i) + t * g.is + c);
+            xr[j] = load_stream<T, V>(static_cast<const T *>(g.x) + t * g.xs + c);
+        }
+    float rate[V], start[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        rate[v] = live ? expf(g.A_log[c + v]) : 0.0f;
+        start[v] = !PACKED && live && g.init ? g.init[(long long)it.row * g.D + c + v] : 0.0f;
+    }
+    if constexpr (PACKED)
+        mark_sequences(g, marks, tile0, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, true,
+                       [&](int s) {
+                           if (!final_states) return;
+                           for (int k = it.blk * 32 * V; k < min((it.blk + 1) * 32 * V, g.D); ++k)
+                               final_states[(long long)s * g.D + k] = g.init ? g.init[(long long)s * g.D + k] : 0.0f;
+                       });
+
+    float a[L][V], b[L][V], A[V], B[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const bool in = live && t0 + j < g.T;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            a[j][v] = 1.0f, b[j][v] = 0.0f;
+            if (in) {
+                const Gate k = gate(to_f32(rr[j].v[v]), to_f32(ir[j].v[v]), rate[v]);
+                a[j][v] = k.a;
+                b[j][v] = k.m * k.si * to_f32(xr[j].v[v]);
+            }
+        }
+        if (PACKED) {
+            const int s = marks.first[w * L + j];
+            if (s >= 0 && in)
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    b[j][v] = fmaf(a[j][v], g.init ? g.init[(long long)s * g.D + c + v] : 0.0f, b[j][v]);
+                    a[j][v] = 0.0f;
+                }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) compose_map<PACKED>(A[v], B[v], a[j][v], b[j][v]);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) sm.run[w][lane * V + v] = make_float2(A[v], B[v]);
+    __syncthreads();
+    float h[V];
+    enter_state<V, W, PACKED>(tl, it, g.D, c, live, w, lane, start, sm, g.status, h);
+    if (!live || t0 >= g.T) return;
+
+    if (chunk_states && t0 % SSD_GLR_CHUNK == 0) {
+        float e[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) e[v] = h[v];
+        if (PACKED) {
+            const int s = marks.first[w * L];
+            if (s >= 0)
+#pragma unroll
+                for (int v = 0; v < V; ++v) e[v] = g.init ? g.init[(long long)s * g.D + c + v] : 0.0f;
+        }
+        store_vec<float, V>(chunk_states + ((long long)it.row * g.nchunk + t0 / SSD_GLR_CHUNK) * g.D + c, e);
+    }
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        if (t0 + j < g.T) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) h[v] = apply_map<PACKED>(a[j][v], b[j][v], h[v]);
+            if (y) store_vec<T, V>(y + (row0 + t0 + j) * g.D + c, h);
+            if (final_states) {
+                const int s = PACKED ? marks.last[w * L + j] : (t0 + j == g.T - 1 ? it.row : -1);
+                if (s >= 0) store_vec<float, V>(final_states + (long long)s * g.D + c, h);
+            }
+        }
+}
+
+// One tile of L W = SSD_GLR_CHUNK tokens, the row's last tile first.  The
+// forward's states come from the chunk state and the runs' maps; the gradient
+// that enters a token from the later ones, c_t = a_t (dy_t + c_{t+1}), is a map
+// of the same kind scanned backwards.
+template <typename T, typename G, int V, int L, int W, bool PACKED>
+__global__ void __launch_bounds__(32 * W, 512 / (32 * W))
+glr_bwd_kernel(GlrArgs g, Tiling tl, const float *__restrict__ chunk_states, const T *__restrict__ dy,
                const float *__restrict__ dfinal, G *__restrict__ dx, G *__restrict__ dr, G *__restrict__ di,
-               float *__restrict__ dA_part, float *__restrict__ dinit)
+               float *__restrict__ dA_part, float *__restrict__ dA, float *__restrict__ dinit)
 {
-    const int c = blockIdx.y * kThreads + threadIdx.x, s = blockIdx.x;
-    const SeqSpan span = seq_span(g, s, blockIdx.y == 0 && threadIdx.x == 0);
-    if (c >= g.D) return;
-    const float rate = expf(g.A_log[c]);
-    float carry = dfinal ? dfinal[(size_t)s * g.D + c] : 0.0f;
-    float dA = 0.0f;
-    const long long row0 = g.cu ? 0 : span.lo;
-    float h[SSD_GLR_CHUNK];                                  // state before each token of a chunk
-    for (long long k = (span.hi - 1 - row0) / SSD_GLR_CHUNK; span.hi > span.lo; --k) {
-        const long long lo = max(row0 + k * SSD_GLR_CHUNK, span.lo);
-        const long long hi = min(row0 + (k + 1) * SSD_GLR_CHUNK, span.hi);
-        float v = lo > span.lo || (lo - row0) % SSD_GLR_CHUNK == 0
-                      ? chunk_states[((g.cu ? 0 : (long long)s * g.nchunk) + k) * g.D + c]
-                      : (g.init ? g.init[(size_t)s * g.D + c] : 0.0f);
-        for (long long t = lo; t < hi; ++t) {
-            h[t - lo] = v;
-            const Gate q = gate(to_f32(static_cast<const T *>(g.r)[t * g.rs + c]),
-                                to_f32(static_cast<const T *>(g.i)[t * g.is + c]), rate);
-            v = fmaf(q.a, v, q.m * q.si * to_f32(static_cast<const T *>(g.x)[t * g.xs + c]));
+    static_assert(L * W == SSD_GLR_CHUNK, "a tile starts at a chunk state");
+    __shared__ ScanSmem<V, W> sm;
+    __shared__ float2 fwd_run[W][32 * V];
+    __shared__ Marks<PACKED ? L * W : 1> marks;
+    __shared__ int slot, is_last;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const Item it = item_of(tl, take_ticket(tl, &slot));
+    const int tile = tl.ntiles - 1 - it.step;
+    const int c = (it.blk * 32 + lane) * V;
+    const bool live = c < g.D;
+    const int tile0 = tile * (L * W), t0 = tile0 + w * L;
+    const long long row0 = (long long)it.row * g.T;
+
+    Vec<T, V> xr[L], rr[L], ir[L], dr_[L];
+#pragma unroll
+    for (int j = 0; j < L; ++j)
+        if (live && t0 + j < g.T) {
+            const long long t = row0 + t0 + j;
+            rr[j] = load_stream<T, V>(static_cast<const T *>(g.r) + t * g.rs + c);
+            ir[j] = load_stream<T, V>(static_cast<const T *>(g.i) + t * g.is + c);
+            xr[j] = load_stream<T, V>(static_cast<const T *>(g.x) + t * g.xs + c);
+            dr_[j] = load_stream<T, V>(dy + t * g.D + c);
         }
-        for (long long t = hi - 1; t >= lo; --t) {
-            const float x = to_f32(static_cast<const T *>(g.x)[t * g.xs + c]);
-            const Gate q = gate(to_f32(static_cast<const T *>(g.r)[t * g.rs + c]),
-                                to_f32(static_cast<const T *>(g.i)[t * g.is + c]), rate);
-            const float gt = to_f32(dy[t * g.D + c]) + carry;
-            const float gm = gt * q.m * q.si;
-            // q dm/dq = q a^2 / m stays finite as q -> 0
-            const float dqq = q.a * (q.q * q.a * q.inv_m * gt * q.si * x - q.q * gt * h[t - lo]);
-            dx[t * g.D + c] = from_f32<G>(gm);
-            di[t * g.D + c] = from_f32<G>(gm * x * q.osi);
-            dr[t * g.D + c] = from_f32<G>(dqq * q.osr);
-            dA += dqq;
-            carry = q.a * gt;
-        }
-        if (lo == span.lo) break;
+    float rate[V], start[V], h[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        rate[v] = live ? expf(g.A_log[c + v]) : 0.0f;
+        start[v] = !PACKED && live && dfinal ? dfinal[(long long)it.row * g.D + c + v] : 0.0f;
+        h[v] = live && tile0 < g.T ? chunk_states[((long long)it.row * g.nchunk + tile) * g.D + c + v] : 0.0f;
     }
-    dA_part[(size_t)s * g.D + c] = dA;
-    if (dinit) dinit[(size_t)s * g.D + c] = carry;
+    if constexpr (PACKED)
+        mark_sequences(g, marks, tile0, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, true,
+                       [&](int s) {
+                           if (!dinit) return;
+                           for (int k = it.blk * 32 * V; k < min((it.blk + 1) * 32 * V, g.D); ++k)
+                               dinit[(long long)s * g.D + k] = dfinal ? dfinal[(long long)s * g.D + k] : 0.0f;
+                       });
+
+    Gate k[L][V];
+    float A[V], B[V], Ar[V], Br[V], dyv[L][V], x[L][V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) A[v] = Ar[v] = 1.0f, B[v] = Br[v] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const bool in = live && t0 + j < g.T;
+        const int s = PACKED && in ? marks.first[w * L + j] : -1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (in) {
+                k[j][v] = gate(to_f32(rr[j].v[v]), to_f32(ir[j].v[v]), rate[v]);
+                x[j][v] = to_f32(xr[j].v[v]);
+                dyv[j][v] = to_f32(dr_[j].v[v]);
+            } else {
+                k[j][v] = Gate{1.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                x[j][v] = dyv[j][v] = 0.0f;
+            }
+            float fa = k[j][v].a, fb = k[j][v].m * k[j][v].si * x[j][v];
+            if (PACKED && s >= 0) {
+                fb = fmaf(fa, g.init ? g.init[(long long)s * g.D + c + v] : 0.0f, fb);
+                fa = 0.0f;
+            }
+            compose_map<PACKED>(A[v], B[v], fa, fb);
+        }
+    }
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j) {
+        const int s = PACKED && live && t0 + j < g.T ? marks.last[w * L + j] : -1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (PACKED && s >= 0) {
+                dyv[j][v] += dfinal ? dfinal[(long long)s * g.D + c + v] : 0.0f;
+                Ar[v] = 0.0f;
+                Br[v] = k[j][v].a * dyv[j][v];
+            } else {
+                const float a = k[j][v].a;
+                compose_map<false>(Ar[v], Br[v], a, a * dyv[j][v]);
+            }
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        fwd_run[w][lane * V + v] = make_float2(A[v], B[v]);
+        sm.run[W - 1 - w][lane * V + v] = make_float2(Ar[v], Br[v]);
+    }
+    __syncthreads();
+    float carry[V];
+    enter_state<V, W, PACKED>(tl, it, g.D, c, live, W - 1 - w, lane, start, sm, g.status, carry);
+    for (int q = 0; q < w; ++q)
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const float2 m = fwd_run[q][lane * V + v];
+            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
+        }
+
+    float before[L][V], dAs[V];
+#pragma unroll
+    for (int j = 0; j < L; ++j) {
+        const int s = PACKED && live && t0 + j < g.T ? marks.first[w * L + j] : -1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (PACKED && s >= 0) h[v] = g.init ? g.init[(long long)s * g.D + c + v] : 0.0f;
+            before[j][v] = h[v];
+            h[v] = fmaf(k[j][v].a, h[v], k[j][v].m * k[j][v].si * x[j][v]);
+        }
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) dAs[v] = 0.0f;
+#pragma unroll
+    for (int j = L - 1; j >= 0; --j) {
+        if (!live || t0 + j >= g.T) continue;
+        const bool cut = PACKED && marks.last[w * L + j] >= 0;
+        float o1[V], o2[V], o3[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const Gate &q = k[j][v];
+            const float gt = cut ? dyv[j][v] : dyv[j][v] + carry[v];
+            const float gs = gt * q.si;
+            o1[v] = gs * q.m;
+            o2[v] = o1[v] * x[j][v] * q.osi;
+            // q dm/dq = q a^2 / m, finite as q -> 0
+            const float dqq = q.q * q.a * (q.a * q.inv_m * gs * x[j][v] - gt * before[j][v]);
+            o3[v] = dqq * q.osr;
+            dAs[v] += dqq;
+            carry[v] = q.a * gt;
+        }
+        const long long at = (row0 + t0 + j) * g.D + c;
+        store_vec<G, V>(dx + at, o1);
+        store_vec<G, V>(di + at, o2);
+        store_vec<G, V>(dr + at, o3);
+        if (dinit) {
+            const int s = PACKED ? marks.first[w * L + j] : (t0 + j == 0 ? it.row : -1);
+            if (s >= 0) store_vec<float, V>(dinit + (long long)s * g.D + c, carry);
+        }
+    }
+
+    // dA_log: over the runs here, over tiles and rows by the channel block's last CTA
+    float *red = &fwd_run[0][0].x;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) red[w * 32 * V + lane * V + v] = dAs[v];
+    __syncthreads();
+    const int total = tl.rows * tl.ntiles, cl = threadIdx.x;
+    float part = 0.0f;
+    if (cl < 32 * V && it.blk * 32 * V + cl < g.D) {
+        for (int q = 0; q < W; ++q) part += red[q * 32 * V + cl];
+        if (total == 1)
+            dA[it.blk * 32 * V + cl] = part;
+        else
+            __stcg(&dA_part[((long long)it.row * tl.ntiles + tile) * g.D + it.blk * 32 * V + cl], part);
+    }
+    if (total == 1) return;
+    __threadfence();
+    __syncthreads();
+    if (threadIdx.x == 0) is_last = atomicAdd(&tl.done[it.blk], 1) == total - 1;
+    __syncthreads();
+    if (!is_last) return;
+    __threadfence();
+    float sum[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
+    if (live)
+        for (int q = w; q < total; q += W)
+#pragma unroll
+            for (int v = 0; v < V; ++v) sum[v] += __ldcg(&dA_part[(long long)q * g.D + c + v]);
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < V; ++v) red[w * 32 * V + lane * V + v] = sum[v];
+    __syncthreads();
+    if (cl < 32 * V && it.blk * 32 * V + cl < g.D) {
+        part = 0.0f;
+        for (int q = 0; q < W; ++q) part += red[q * 32 * V + cl];
+        dA[it.blk * 32 * V + cl] = part;
+    }
 }
 
-__global__ void __launch_bounds__(kThreads) glr_dA_kernel(int n, int D, const float *__restrict__ part, float *__restrict__ dA)
+// Rows without tokens: final states (initial-state gradients) are copies.
+__global__ void glr_copy_kernel(long long n, const float *__restrict__ from, float *__restrict__ to)
 {
-    const int c = blockIdx.x * kThreads + threadIdx.x;
-    if (c >= D) return;
-    float v = 0.0f;
-    for (int k = 0; k < n; ++k) v += part[(size_t)k * D + c];
-    dA[c] = v;
+    for (long long k = (long long)blockIdx.x * blockDim.x + threadIdx.x; k < n; k += (long long)gridDim.x * blockDim.x)
+        to[k] = from ? from[k] : 0.0f;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-glr_step_kernel(long long n, int D, const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
+constexpr int kStepThreads = 128;
+
+template <typename T, int V>
+__global__ void __launch_bounds__(kStepThreads)
+glr_step_kernel(int rows, int D, const T *__restrict__ x, const T *__restrict__ r, const T *__restrict__ i,
                 long long xs, long long rs, long long is, const float *__restrict__ A_log, float *__restrict__ state,
                 T *__restrict__ y)
 {
-    const long long k = (long long)blockIdx.x * kThreads + threadIdx.x;
+    const unsigned per = D / V;
+    const unsigned long long n = (unsigned long long)rows * per;
+    const unsigned long long k = (unsigned long long)blockIdx.x * kStepThreads + threadIdx.x;
     if (k >= n) return;
-    const long long row = k / D;
-    const int c = (int)(k - row * D);
-    const Gate q = gate(to_f32(r[row * rs + c]), to_f32(i[row * is + c]), expf(A_log[c]));
-    const float h = fmaf(q.a, state[k], q.m * q.si * to_f32(x[row * xs + c]));
-    state[k] = h;
-    y[k] = from_f32<T>(h);
+    const unsigned row = n >> 32 ? (unsigned)(k / per) : (unsigned)k / per;
+    const unsigned c = (unsigned)(k - (unsigned long long)row * per) * V;
+    const Vec<T, V> xv = load_stream<T, V>(x + row * xs + c), rv = load_stream<T, V>(r + row * rs + c),
+                    iv = load_stream<T, V>(i + row * is + c);
+    const size_t at = (size_t)row * D + c;
+    float h[V], al[V];
+    load_f32<V>(state + at, h);
+    load_f32<V>(A_log + c, al);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        const Gate q = gate(to_f32(rv.v[v]), to_f32(iv.v[v]), expf(al[v]));
+        h[v] = fmaf(q.a, h[v], q.m * q.si * to_f32(xv.v[v]));
+    }
+    store_vec<float, V>(state + at, h);
+    store_vec<T, V>(y + at, h);
 }
+
+// ---------------------------------------------------------------- host side
 
 bool valid_dtype(ssd_dtype t) { return t == SSD_DTYPE_F32 || t == SSD_DTYPE_BF16; }
 size_t elem_size(ssd_dtype t) { return t == SSD_DTYPE_BF16 ? 2 : 4; }
@@ -115,8 +544,10 @@ ssd_status validate(const ssd_glr_params *p)
     if (p->x_stride < p->channels || p->r_stride < p->channels || p->i_stride < p->channels)
         return SSD_ERR_INVALID_ARG;
     const int64_t lim = int64_t(1) << 31;
+    // 32-bit tokens and work items (64 tokens by 32 channels at the least)
     if ((int64_t)p->batch * p->seqlen >= lim - 1024 || p->x_stride >= lim || p->r_stride >= lim || p->i_stride >= lim ||
-        p->num_seqs > (1 << 20) || p->channels >= (1 << 22))
+        p->channels > lim - 1024 || p->num_seqs > (1 << 20) ||
+        (int64_t)p->batch * ((p->seqlen + 63) / 64) * ((p->channels + 31) / 32) >= lim)
         return SSD_ERR_UNSUPPORTED;
     return SSD_OK;
 }
@@ -137,23 +568,130 @@ GlrArgs args_of(const ssd_glr_params &p, const void *x, const void *r, const voi
     return g;
 }
 
-template <typename T>
-cudaError_t fwd(const GlrArgs &g, void *y, float *fin, float *chunks, cudaStream_t st)
+// Tile shapes: tokens a tile; channels a block is 32 V, V = 1 or 2.
+constexpr int kFwdL = 16, kFwdW = 8, kBwdL = 4, kBwdW = 16;
+
+// Workspace of one scan: status word, counters and flags (cleared together),
+// then maps and states.  Sized for V = 1, the most channel blocks.
+struct Scan {
+    Tiling tl;
+    size_t clear, bytes;
+};
+
+Scan scan_of(const ssd_glr_params &p, int tile_tokens, int V, bool bwd, char *ws)
 {
-    const dim3 grid(g.nseq, (g.D + kThreads - 1) / kThreads);
-    glr_fwd_kernel<T><<<grid, kThreads, 0, st>>>(g, static_cast<T *>(y), fin, chunks);
+    Scan s{};
+    Tiling &t = s.tl;
+    t.rows = p.batch;
+    t.ntiles = (int)(((int64_t)p.seqlen + tile_tokens - 1) / tile_tokens);
+    t.nblk = (p.channels + 32 * V - 1) / (32 * V);
+    const size_t groups = (size_t)t.rows * ((t.ntiles + kGroup - 1) / kGroup);
+    const size_t items = (size_t)t.rows * t.ntiles * t.nblk;
+    size_t off = sizeof(int);
+    const auto take = [&](size_t n) { const size_t at = off; off += n * sizeof(int); return reinterpret_cast<int *>(ws + at); };
+    t.ticket = take(1);
+    if (bwd) t.done = take(t.nblk);
+    if (t.ntiles > 1) {
+        t.map_flag = take(items);
+        t.state_flag = take(groups * t.nblk);
+    }
+    s.clear = off;
+    off = align_up(off);
+    if (t.ntiles > 1) {
+        t.maps = reinterpret_cast<float2 *>(ws + off);
+        off = align_up(off + (size_t)t.rows * t.ntiles * p.channels * sizeof(float2));
+        t.states = reinterpret_cast<float *>(ws + off);
+        off = align_up(off + groups * p.channels * sizeof(float));
+    }
+    s.bytes = off;
+    return s;
+}
+
+struct BwdLayout {
+    size_t scan, part, chunks, total;
+};
+
+BwdLayout bwd_layout(const ssd_glr_params &p, bool with_chunks)
+{
+    BwdLayout l{};
+    const size_t n = (size_t)p.batch * chunks_of(p) * p.channels * sizeof(float);
+    l.part = scan_of(p, kBwdL * kBwdW, 1, true, nullptr).bytes;
+    l.chunks = align_up(l.part + n);
+    l.total = with_chunks ? l.chunks : align_up(l.chunks + n);
+    const size_t f = scan_of(p, kFwdL * kFwdW, 1, false, nullptr).bytes;
+    if (!with_chunks && f > l.chunks) {          // the forward's scan runs first, in the same place
+        l.chunks = f;
+        l.total = align_up(f + n);
+    }
+    return l;
+}
+
+// Channels a lane: as many as the rows' alignment allows.
+int width_of(const ssd_glr_params &p, std::initializer_list<const void *> io, std::initializer_list<const void *> f32)
+{
+    const size_t es = elem_size(p.io_dtype);
+    if (p.channels % 2 || p.x_stride % 2 || p.r_stride % 2 || p.i_stride % 2) return 1;
+    for (const void *q : io)
+        if (!aligned(q, 2 * es)) return 1;
+    for (const void *q : f32)
+        if (!aligned(q, 8)) return 1;
+    return 2;
+}
+
+template <typename T, int V>
+void launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((size_t)tl.rows * tl.ntiles * tl.nblk);
+    if (g.cu)
+        glr_fwd_kernel<T, V, kFwdL, kFwdW, true><<<grid, 32 * kFwdW, 0, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+    else
+        glr_fwd_kernel<T, V, kFwdL, kFwdW, false><<<grid, 32 * kFwdW, 0, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+}
+
+cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_t st)
+{
+    const long long n = (long long)g.nseq * g.D;
+    const unsigned grid = (unsigned)(n < 256 * 1024 ? (n + 255) / 256 : 1024);
+    glr_copy_kernel<<<grid, 256, 0, st>>>(n, from, to);
     return cudaGetLastError();
 }
 
-template <typename T, typename G>
-cudaError_t bwd(const GlrArgs &g, const float *chunks, const void *dy, const float *dfinal, void *dx, void *dr, void *di,
-                float *part, float *dA, float *dinit, cudaStream_t st)
+cudaError_t run_fwd(const ssd_glr_params &p, const GlrArgs &g, void *y, float *fin, float *chunks, char *ws,
+                    cudaStream_t st)
 {
-    const dim3 grid(g.nseq, (g.D + kThreads - 1) / kThreads);
-    glr_bwd_kernel<T, G><<<grid, kThreads, 0, st>>>(g, chunks, static_cast<const T *>(dy), dfinal, static_cast<G *>(dx),
-                                                    static_cast<G *>(dr), static_cast<G *>(di), part, dinit);
-    glr_dA_kernel<<<grid.y, kThreads, 0, st>>>(g.nseq, g.D, part, dA);
+    const int V = width_of(p, {g.x, g.r, g.i, y}, {fin, chunks});
+    const Scan s = scan_of(p, kFwdL * kFwdW, V, false, ws);
+    const cudaError_t e = cudaMemsetAsync(ws, 0, s.clear, st);
+    if (e != cudaSuccess) return e;
+    if (p.seqlen == 0) return fin ? run_copy(g, g.init, fin, st) : cudaSuccess;
+    const bool bf = p.io_dtype == SSD_DTYPE_BF16;
+    if (bf && V == 2) launch_fwd<__nv_bfloat16, 2>(g, s.tl, y, fin, chunks, st);
+    else if (bf) launch_fwd<__nv_bfloat16, 1>(g, s.tl, y, fin, chunks, st);
+    else if (V == 2) launch_fwd<float, 2>(g, s.tl, y, fin, chunks, st);
+    else launch_fwd<float, 1>(g, s.tl, y, fin, chunks, st);
     return cudaGetLastError();
+}
+
+struct BwdArgs {
+    const float *chunks;
+    const void *dy;
+    const float *dfinal;
+    void *dx, *dr, *di;
+    float *part, *dA, *dinit;
+};
+
+template <typename T, typename G, int V>
+void launch_bwd(const GlrArgs &g, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
+{
+    const unsigned grid = (unsigned)((size_t)tl.rows * tl.ntiles * tl.nblk);
+    const T *dy = static_cast<const T *>(b.dy);
+    G *dx = static_cast<G *>(b.dx), *dr = static_cast<G *>(b.dr), *di = static_cast<G *>(b.di);
+    if (g.cu)
+        glr_bwd_kernel<T, G, V, kBwdL, kBwdW, true><<<grid, 32 * kBwdW, 0, st>>>(g, tl, b.chunks, dy, b.dfinal, dx, dr,
+                                                                                 di, b.part, b.dA, b.dinit);
+    else
+        glr_bwd_kernel<T, G, V, kBwdL, kBwdW, false><<<grid, 32 * kBwdW, 0, st>>>(g, tl, b.chunks, dy, b.dfinal, dx, dr,
+                                                                                  di, b.part, b.dA, b.dinit);
 }
 
 }  // namespace
@@ -165,15 +703,12 @@ extern "C" {
 
 size_t ssd_glr_fwd_workspace_size(const ssd_glr_params *p)
 {
-    return validate(p) == SSD_OK ? kAlign : 0;
+    return validate(p) == SSD_OK ? scan_of(*p, kFwdL * kFwdW, 1, false, nullptr).bytes : 0;
 }
 
 size_t ssd_glr_bwd_workspace_size(const ssd_glr_params *p, int with_chunk_states)
 {
-    if (validate(p) != SSD_OK) return 0;
-    size_t n = kAlign + align_up((size_t)nseq_of(*p) * p->channels * sizeof(float));
-    if (!with_chunk_states) n += align_up((size_t)p->batch * chunks_of(*p) * p->channels * sizeof(float));
-    return n;
+    return validate(p) == SSD_OK ? bwd_layout(*p, with_chunk_states != 0).total : 0;
 }
 
 ssd_status ssd_glr_fwd(const ssd_glr_params *p, const void *x, const void *r, const void *i, const float *A_log,
@@ -191,11 +726,9 @@ ssd_status ssd_glr_fwd(const ssd_glr_params *p, const void *x, const void *r, co
     for (const void *q : {(const void *)A_log, (const void *)initial_states, (const void *)cu_seqlens,
                           (const void *)final_states, (const void *)chunk_states})
         if (!aligned(q, 4)) return SSD_ERR_INVALID_ARG;
-    cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(int), st) != cudaSuccess) return SSD_ERR_CUDA;
     const GlrArgs g = args_of(*p, x, r, i, A_log, initial_states, cu_seqlens, workspace);
-    const cudaError_t e = p->io_dtype == SSD_DTYPE_BF16 ? fwd<__nv_bfloat16>(g, y, final_states, chunk_states, st)
-                                                        : fwd<float>(g, y, final_states, chunk_states, st);
+    const cudaError_t e = run_fwd(*p, g, y, final_states, chunk_states, static_cast<char *>(workspace),
+                                  static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
@@ -220,26 +753,35 @@ ssd_status ssd_glr_bwd(const ssd_glr_params *p, const void *x, const void *r, co
                           (const void *)dinitial_states})
         if (!aligned(q, 4)) return SSD_ERR_INVALID_ARG;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (cudaMemsetAsync(workspace, 0, sizeof(int), st) != cudaSuccess) return SSD_ERR_CUDA;
     const GlrArgs g = args_of(*p, x, r, i, A_log, initial_states, cu_seqlens, workspace);
     char *ws = static_cast<char *>(workspace);
-    float *part = reinterpret_cast<float *>(ws + kAlign);
-    const float *chunks = chunk_states;
-    const bool bf = p->io_dtype == SSD_DTYPE_BF16;
-    if (!chunks) {
-        float *c = reinterpret_cast<float *>(ws + kAlign + align_up((size_t)g.nseq * g.D * sizeof(float)));
-        const cudaError_t e = bf ? fwd<__nv_bfloat16>(g, nullptr, nullptr, c, st) : fwd<float>(g, nullptr, nullptr, c, st);
-        if (e != cudaSuccess) return SSD_ERR_CUDA;
-        chunks = c;
+    const BwdLayout l = bwd_layout(*p, chunk_states != nullptr);
+    BwdArgs b{chunk_states, dy, dfinal_states, dx, dr, di, reinterpret_cast<float *>(ws + l.part), dA_log,
+              dinitial_states};
+    if (!chunk_states && p->seqlen > 0) {
+        float *c = reinterpret_cast<float *>(ws + l.chunks);
+        if (run_fwd(*p, g, nullptr, nullptr, c, ws, st) != cudaSuccess) return SSD_ERR_CUDA;
+        b.chunks = c;
     }
-    cudaError_t e;
-    if (bf && p->grad_dtype == SSD_DTYPE_BF16)
-        e = bwd<__nv_bfloat16, __nv_bfloat16>(g, chunks, dy, dfinal_states, dx, dr, di, part, dA_log, dinitial_states, st);
-    else if (bf)
-        e = bwd<__nv_bfloat16, float>(g, chunks, dy, dfinal_states, dx, dr, di, part, dA_log, dinitial_states, st);
-    else
-        e = bwd<float, float>(g, chunks, dy, dfinal_states, dx, dr, di, part, dA_log, dinitial_states, st);
-    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    const size_t ga = 2 * gs;
+    int V = width_of(*p, {x, r, i, dy}, {dinitial_states});
+    if (!aligned(dx, ga) || !aligned(dr, ga) || !aligned(di, ga)) V = 1;
+    const Scan s = scan_of(*p, kBwdL * kBwdW, V, true, ws);
+    if (cudaMemsetAsync(ws, 0, s.clear, st) != cudaSuccess) return SSD_ERR_CUDA;
+    if (p->seqlen == 0) {
+        if (cudaMemsetAsync(dA_log, 0, p->channels * sizeof(float), st) != cudaSuccess) return SSD_ERR_CUDA;
+        const cudaError_t e = dinitial_states ? run_copy(g, dfinal_states, dinitial_states, st) : cudaSuccess;
+        return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    }
+    typedef __nv_bfloat16 H;
+    const bool bf = p->io_dtype == SSD_DTYPE_BF16, gb = p->grad_dtype == SSD_DTYPE_BF16;
+    if (bf && gb && V == 2) launch_bwd<H, H, 2>(g, s.tl, b, st);
+    else if (bf && gb) launch_bwd<H, H, 1>(g, s.tl, b, st);
+    else if (bf && V == 2) launch_bwd<H, float, 2>(g, s.tl, b, st);
+    else if (bf) launch_bwd<H, float, 1>(g, s.tl, b, st);
+    else if (V == 2) launch_bwd<float, float, 2>(g, s.tl, b, st);
+    else launch_bwd<float, float, 1>(g, s.tl, b, st);
+    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_glr_step(const ssd_glr_step_params *p, const void *x, const void *r, const void *i, const float *A_log,
@@ -253,20 +795,24 @@ ssd_status ssd_glr_step(const ssd_glr_step_params *p, const void *x, const void 
     if (!x || !r || !i || !A_log || !state || !y || !aligned(x, es) || !aligned(r, es) || !aligned(i, es) ||
         !aligned(y, es) || !aligned(A_log, 4) || !aligned(state, 4))
         return SSD_ERR_INVALID_ARG;
-    const long long n = (long long)p->batch * p->channels, blocks = (n + kThreads - 1) / kThreads;
+    const bool two = p->channels % 2 == 0 && p->x_stride % 2 == 0 && p->r_stride % 2 == 0 && p->i_stride % 2 == 0 &&
+                     aligned(x, 2 * es) && aligned(r, 2 * es) && aligned(i, 2 * es) && aligned(y, 2 * es) &&
+                     aligned(A_log, 8) && aligned(state, 8);
+    const long long n = (long long)p->batch * (p->channels / (two ? 2 : 1));
+    const long long blocks = (n + kStepThreads - 1) / kStepThreads;
     if (blocks > 0x7fffffffLL) return SSD_ERR_UNSUPPORTED;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (p->io_dtype == SSD_DTYPE_BF16) {
-        typedef __nv_bfloat16 T;
-        glr_step_kernel<T><<<(unsigned)blocks, kThreads, 0, st>>>(
-            n, p->channels, static_cast<const T *>(x), static_cast<const T *>(r), static_cast<const T *>(i),
+    const auto go = [&](auto kernel, auto *tag) {
+        typedef std::remove_pointer_t<decltype(tag)> T;
+        kernel<<<(unsigned)blocks, kStepThreads, 0, st>>>(
+            p->batch, p->channels, static_cast<const T *>(x), static_cast<const T *>(r), static_cast<const T *>(i),
             p->x_stride, p->r_stride, p->i_stride, A_log, state, static_cast<T *>(y));
-    } else {
-        typedef float T;
-        glr_step_kernel<T><<<(unsigned)blocks, kThreads, 0, st>>>(
-            n, p->channels, static_cast<const T *>(x), static_cast<const T *>(r), static_cast<const T *>(i),
-            p->x_stride, p->r_stride, p->i_stride, A_log, state, static_cast<T *>(y));
-    }
+    };
+    typedef __nv_bfloat16 H;
+    if (p->io_dtype == SSD_DTYPE_BF16 && two) go(glr_step_kernel<H, 2>, (H *)nullptr);
+    else if (p->io_dtype == SSD_DTYPE_BF16) go(glr_step_kernel<H, 1>, (H *)nullptr);
+    else if (two) go(glr_step_kernel<float, 2>, (float *)nullptr);
+    else go(glr_step_kernel<float, 1>, (float *)nullptr);
     return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 

@@ -87,19 +87,105 @@ __device__ __forceinline__ Gate gate(float r, float i, float rate)
     return g;
 }
 
-struct SeqSpan {
-    long long lo, hi;           // tokens of the sequence on the flattened axis, 0 <= lo <= hi
+// ---------------------------------------------------------------- vectors of V adjacent channels
+template <typename T, int V>
+struct alignas(sizeof(T) * V) Vec {
+    T v[V];
 };
 
-// Tokens of sequence s; a cu_seqlens that is not 0 = c0 <= ... <= T is recorded
-// (`report`) and clamped, so that no access leaves the buffers.
-__device__ __forceinline__ SeqSpan seq_span(const GlrArgs &g, int s, bool report)
+// Read once, so it is kept out of L1.
+template <typename T, int V>
+__device__ __forceinline__ Vec<T, V> load_stream(const T *p)
 {
-    if (!g.cu) return {(long long)s * g.T, (long long)(s + 1) * g.T};
-    const int a = g.cu[s], b = g.cu[s + 1];
-    if (report && (a > b || (s == 0 && a != 0) || (s == g.nseq - 1 && b != g.T))) set_status(g.status, kDevBadSeqlens);
-    const int lo = min(max(a, 0), g.T);
-    return {lo, min(max(b, lo), g.T)};
+    union {
+        Vec<T, V> v;
+        uint16_t h;
+        uint32_t w[4];
+    } u;
+    if constexpr (sizeof(T) * V == 2)
+        asm volatile("ld.global.nc.L1::no_allocate.u16 %0, [%1];" : "=h"(u.h) : "l"(p));
+    else if constexpr (sizeof(T) * V == 4)
+        asm volatile("ld.global.nc.L1::no_allocate.u32 %0, [%1];" : "=r"(u.w[0]) : "l"(p));
+    else if constexpr (sizeof(T) * V == 8)
+        asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(u.w[0]), "=r"(u.w[1]) : "l"(p));
+    else
+        asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(u.w[0]), "=r"(u.w[1]), "=r"(u.w[2]), "=r"(u.w[3]) : "l"(p));
+    return u.v;
+}
+
+template <typename T, int V>
+__device__ __forceinline__ void store_vec(T *p, const float (&f)[V])
+{
+    Vec<T, V> o;
+#pragma unroll
+    for (int k = 0; k < V; ++k) o.v[k] = from_f32<T>(f[k]);
+    *reinterpret_cast<Vec<T, V> *>(p) = o;
+}
+
+template <int V>
+__device__ __forceinline__ void load_f32(const float *p, float (&f)[V])
+{
+    const Vec<float, V> o = *reinterpret_cast<const Vec<float, V> *>(p);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = o.v[k];
+}
+
+// ---------------------------------------------------------------- maps h -> A h + B
+// A row's updates compose to such maps.  In a packed batch the first token of a
+// sequence forgets what came before it: there A is exactly 0, and "A h" is left
+// out rather than multiplied, so that a state that is not finite stays in its
+// own sequence.
+template <bool PACKED>
+__device__ __forceinline__ float apply_map(float A, float B, float h)
+{
+    const float v = fmaf(A, h, B);
+    return PACKED && A == 0.0f ? B : v;
+}
+
+// (A, B) <- (A2, B2) after (A, B)
+template <bool PACKED>
+__device__ __forceinline__ void compose_map(float &A, float &B, float A2, float B2)
+{
+    const bool cut = PACKED && A2 == 0.0f;
+    B = cut ? B2 : fmaf(A2, B, B2);
+    A = cut ? 0.0f : A * A2;
+}
+
+// ---------------------------------------------------------------- waits between CTAs
+__device__ __forceinline__ int ld_acquire(const int *p)
+{
+    int v;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(int *p, int v)
+{
+    asm volatile("st.release.gpu.global.s32 [%0], %1;" ::"l"(p), "r"(v) : "memory");
+}
+__device__ __forceinline__ uint64_t now_ns()
+{
+    uint64_t t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+
+// Until *flag is set; after 2 s, or as soon as another wait of the call has
+// given up, records the timeout and returns false.
+__device__ __forceinline__ bool wait_flag(const int *flag, int *status)
+{
+    if (ld_acquire(flag)) return true;
+    const uint64_t t0 = now_ns();
+    for (uint32_t it = 1;; ++it) {
+        if (ld_acquire(flag)) return true;
+        if ((it & 127u) == 0) {
+            if (*reinterpret_cast<volatile int *>(status) == kDevTimeout) return false;
+            if (now_ns() - t0 > 2000000000ull) {
+                atomicExch(status, kDevTimeout);
+                return false;
+            }
+        }
+    }
 }
 
 }  // namespace ssd
