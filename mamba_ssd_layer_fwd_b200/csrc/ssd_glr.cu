@@ -17,6 +17,8 @@
 // kGroup tiles, published by that group's last tile, and the maps of the tiles
 // since, always in the same order: results do not depend on timing, and the
 // chain of dependent waits is ntiles / kGroup long.
+#include <algorithm>
+#include <atomic>
 #include <initializer_list>
 #include <type_traits>
 
@@ -33,8 +35,10 @@ struct Tiling {
     int ntiles, nblk, rows;         // tiles of a row, channel blocks, rows
     int *ticket, *done;             // work counter; per channel block: finished CTAs (backward)
     int *map_flag, *state_flag;     // [item], [row][group][blk]
-    float2 *maps;                   // [row][tile][D]
-    float *states;                  // [row][group][D]
+    float4 *maps;                   // [row][tile][nblk * 32]: of channel pairs
+    float2 *states;                 // [row][group][nblk * 32]
+    float2 *maps1;                  // [row][tile][D]
+    float *states1;
 };
 
 // The row's position of the CTA's tile, counted along the direction of the scan.
@@ -133,7 +137,7 @@ __device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, in
                 if (live) {
 #pragma unroll
                     for (int v = 0; v < V; ++v)
-                        __stcg(&tl.maps[(row_tile + it.step) * D + c + v], make_float2(A[v], B[v]));
+                        __stcg(&tl.maps1[(row_tile + it.step) * D + c + v], make_float2(A[v], B[v]));
                 }
                 __threadfence();
                 __syncwarp();
@@ -152,8 +156,8 @@ __device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, in
                 float2 m[2][V];
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
-                    m[0][v] = __ldcg(&tl.maps[(row_tile + t0) * D + c + v]);
-                    m[1][v] = cnt > 1 ? __ldcg(&tl.maps[(row_tile + t0 + 1) * D + c + v]) : make_float2(1.0f, 0.0f);
+                    m[0][v] = __ldcg(&tl.maps1[(row_tile + t0) * D + c + v]);
+                    m[1][v] = cnt > 1 ? __ldcg(&tl.maps1[(row_tile + t0 + 1) * D + c + v]) : make_float2(1.0f, 0.0f);
                 }
 #pragma unroll
                 for (int v = 0; v < V; ++v) {
@@ -168,7 +172,7 @@ __device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, in
             const long long at = (long long)it.row * ngroups + group - 1;
             const bool ok = wait_flag(&tl.state_flag[at * tl.nblk + it.blk], status);
 #pragma unroll
-            for (int v = 0; v < V; ++v) sm.state[lane * V + v] = ok && live ? __ldcg(&tl.states[at * D + c + v]) : 0.0f;
+            for (int v = 0; v < V; ++v) sm.state[lane * V + v] = ok && live ? __ldcg(&tl.states1[at * D + c + v]) : 0.0f;
         }
         __syncthreads();
     }
@@ -193,7 +197,7 @@ __device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, in
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const float2 m = sm.run[W - 1][lane * V + v];
-                __stcg(&tl.states[at * D + c + v], apply_map<PACKED>(m.x, m.y, h[v]));
+                __stcg(&tl.states1[at * D + c + v], apply_map<PACKED>(m.x, m.y, h[v]));
             }
         }
         __threadfence();
@@ -210,102 +214,232 @@ __device__ __forceinline__ int take_ticket(const Tiling &tl, int *slot)
     return *slot;
 }
 
-// y (NULL: chunk states only), final_states and chunk_states may be NULL
-template <typename T, int V, int L, int W, bool PACKED>
-__global__ void __launch_bounds__(32 * W, 512 / (32 * W))
+// ---------------------------------------------------------------- scans over pairs of channels
+// A CTA of W warps walks tiles of L W tokens by 64 channels: warp w has the
+// tile's run w of L tokens, a lane two adjacent channels.
+constexpr int kL = 8, kW = 8, kTile = kL * kW, kStages = 2;
+
+// Maps as (A, B) of a channel pair.
+__device__ __forceinline__ float4 pack_map(F2 A, F2 B)
+{
+    float4 m;
+    split(A, m.x, m.y), split(B, m.z, m.w);
+    return m;
+}
+__device__ __forceinline__ F2 map_A(float4 m) { return f2(m.x, m.y); }
+__device__ __forceinline__ F2 map_B(float4 m) { return f2(m.z, m.w); }
+
+struct Exchange {
+    float4 run[kW][32];             // maps of the runs, in scan order
+    float4 tile[kGroup / 2][32];    // maps of the group's earlier tiles, by pairs
+    float2 state[32];               // state after the group before
+};
+
+// The exchange between the tiles of a row.  ex.run holds the runs' maps (and a
+// barrier has been passed since); publishes the tile's map (and, for a group's
+// last tile, the state after it) and returns the state entering run w of the
+// scan.  `start` is the state entering the row.
+template <bool PACKED>
+__device__ __forceinline__ F2 enter_state(const Tiling &tl, const Item &it, int w, int lane, F2 start, Exchange &ex,
+                                          int *status)
+{
+    const int in_group = it.step % kGroup, group = it.step / kGroup;
+    const long long row_tile = (long long)it.row * tl.ntiles;
+    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup, pair0 = it.blk * 32 + lane, npairs = tl.nblk * 32;
+    if (tl.ntiles > 1) {
+        if (w == 0 && it.step + 1 < tl.ntiles) {
+            F2 A = f2(1.0f), B = f2(0.0f);
+#pragma unroll
+            for (int k = 0; k < kW; ++k) {
+                const float4 m = ex.run[k][lane];
+                compose_map<PACKED>(A, B, map_A(m), map_B(m));
+            }
+            __stcg(&tl.maps[(row_tile + it.step) * npairs + pair0], pack_map(A, B));
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) st_release(&tl.map_flag[(row_tile + it.step) * tl.nblk + it.blk], 1);
+        }
+        if (w * 2 < in_group) {                     // kGroup / 2 = kW pairs
+            static_assert(kGroup / 2 <= kW, "one pair of tiles a warp");
+            const int t0 = group * kGroup + w * 2;
+            const bool two = w * 2 + 1 < in_group;
+            bool ok = wait_flag(&tl.map_flag[(row_tile + t0) * tl.nblk + it.blk], status);
+            if (ok && two) ok = wait_flag(&tl.map_flag[(row_tile + t0 + 1) * tl.nblk + it.blk], status);
+            F2 A = f2(1.0f), B = f2(0.0f);
+            if (ok) {
+                const float4 *m = &tl.maps[(row_tile + t0) * npairs + pair0];
+                const float4 m0 = __ldcg(m), m1 = two ? __ldcg(m + npairs) : make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+                A = map_A(m0), B = map_B(m0);
+                compose_map<PACKED>(A, B, map_A(m1), map_B(m1));
+            }
+            ex.tile[w][lane] = pack_map(A, B);
+        }
+        if (w == kW - 1 && group > 0) {
+            const long long at = (long long)it.row * ngroups + group - 1;
+            const bool ok = wait_flag(&tl.state_flag[at * tl.nblk + it.blk], status);
+            ex.state[lane] = ok ? __ldcg(&tl.states[at * npairs + pair0]) : make_float2(0.0f, 0.0f);
+        }
+        __syncthreads();
+    }
+    F2 h = group > 0 ? shown(ex.state[lane]) : start;
+    for (int k = 0; k * 2 < in_group; ++k) {
+        const float4 m = ex.tile[k][lane];
+        h = apply_map<PACKED>(map_A(m), map_B(m), h);
+    }
+    for (int k = 0; k < w; ++k) {
+        const float4 m = ex.run[k][lane];
+        h = apply_map<PACKED>(map_A(m), map_B(m), h);
+    }
+    if (w == kW - 1 && in_group == kGroup - 1 && it.step + 1 < tl.ntiles &&
+        *reinterpret_cast<volatile int *>(status) != kDevTimeout) {
+        const long long at = (long long)it.row * ngroups + group;
+        const float4 m = ex.run[w][lane];
+        float2 o;
+        split(apply_map<PACKED>(map_A(m), map_B(m), h), o.x, o.y);
+        __stcg(&tl.states[at * npairs + pair0], o);
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) st_release(&tl.state_flag[at * tl.nblk + it.blk], 1);
+    }
+    return h;
+}
+
+// Copies a run's tokens [t0, t0 + kL) of one array, channels c0 .. c0 + 63, to
+// dst[kL][64]; zeros outside the row or the channels.  COPY is what the rows'
+// alignment allows: 16 bytes, two elements, or one.  A warp's work.
+template <typename T, int COPY>
+__device__ __forceinline__ void stage_run(T *dst, const T *src, long long stride, int t0, int T_, int c0, int D, int lane)
+{
+    constexpr int N = COPY / sizeof(T);             // channels of a copy
+    constexpr int PER = 64 / N;                     // copies of a token
+#pragma unroll
+    for (int k = 0; k < kL * PER / 32; ++k) {
+        const int id = k * 32 + lane, row = id / PER, c = id % PER * N;
+        const bool in = t0 + row < T_ && c0 + c < D;
+        const T *from = in ? src + (long long)(t0 + row) * stride + c0 + c : src;
+        if constexpr (COPY >= 4)
+            copy_async<COPY>(dst + row * 64 + c, from, in);
+        else
+            dst[row * 64 + c] = in ? *from : from_f32<T>(0.0f);
+    }
+}
+
+template <typename T> struct FwdSmem {
+    T in[kStages][kW][3][kL][64];   // r, i, x
+    float A_log[kStages][kW][64];
+    Exchange ex[2];
+    Marks<kTile> marks[2];
+    int slot[4];
+};
+
+// y (NULL: chunk states only), final_states and chunk_states may be NULL.
+//
+// CTAs stay on their SM and take tile after tile.  Each warp copies its own
+// runs, kStages tiles ahead, so HBM reads go on while the CTA computes and
+// waits for other tiles; the ticket of the tile after next is drawn while this
+// one is computed.
+template <typename T, int COPY, bool PACKED>
+__global__ void __launch_bounds__(32 * kW, sizeof(T) == 2 ? 3 : 2)
 glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ final_states,
                float *__restrict__ chunk_states)
 {
-    __shared__ ScanSmem<V, W> sm;
-    __shared__ Marks<PACKED ? L * W : 1> marks;
-    __shared__ int slot;
+    extern __shared__ __align__(16) char smem_raw[];
+    FwdSmem<T> &sm = *reinterpret_cast<FwdSmem<T> *>(smem_raw);
+    constexpr bool PAIR = COPY > sizeof(T);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const Item it = item_of(tl, take_ticket(tl, &slot));
-    const int c = (it.blk * 32 + lane) * V;
-    const bool live = c < g.D;
-    const int tile0 = it.step * (L * W), t0 = tile0 + w * L;       // token in the row
-    const long long row0 = (long long)it.row * g.T;                // token of the row's start on the flat axis
+    const int total = tl.rows * tl.ntiles * tl.nblk;
 
-    Vec<T, V> xr[L], rr[L], ir[L];
-#pragma unroll
-    for (int j = 0; j < L; ++j)
-        if (live && t0 + j < g.T) {
-            const long long t = row0 + t0 + j;
-            rr[j] = load_stream<T, V>(static_cast<const T *>(g.r) + t * g.rs + c);
-            ir[j] = load_stream<T, V>(static_cast<const T *>(g.i) + t * g.is + c);
-            xr[j] = load_stream<T, V>(static_cast<const T *>(g.x) + t * g.xs + c);
+    const auto fetch = [&](int ticket, int stage) {
+        if (ticket < total) {
+            const Item it = item_of(tl, ticket);
+            const int t0 = it.step * kTile + w * kL, c0 = it.blk * 64, c = c0 + 2 * lane;
+            const long long row0 = (long long)it.row * g.T;
+            stage_run<T, COPY>(sm.in[stage][w][0][0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
+            stage_run<T, COPY>(sm.in[stage][w][1][0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
+            stage_run<T, COPY>(sm.in[stage][w][2][0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
+            copy_async<4>(&sm.A_log[stage][w][2 * lane], g.A_log + min(c, g.D - 1), c < g.D);
+            copy_async<4>(&sm.A_log[stage][w][2 * lane + 1], g.A_log + min(c + 1, g.D - 1), c + 1 < g.D);
         }
-    float rate[V], start[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        rate[v] = live ? expf(g.A_log[c + v]) : 0.0f;
-        start[v] = !PACKED && live && g.init ? g.init[(long long)it.row * g.D + c + v] : 0.0f;
-    }
-    if constexpr (PACKED)
-        mark_sequences(g, marks, tile0, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, true,
-                       [&](int s) {
-                           if (!final_states) return;
-                           for (int k = it.blk * 32 * V; k < min((it.blk + 1) * 32 * V, g.D); ++k)
-                               final_states[(long long)s * g.D + k] = g.init ? g.init[(long long)s * g.D + k] : 0.0f;
-                       });
+        copy_commit();
+    };
 
-    float a[L][V], b[L][V], A[V], B[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const bool in = live && t0 + j < g.T;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            a[j][v] = 1.0f, b[j][v] = 0.0f;
-            if (in) {
-                const Gate k = gate(to_f32(rr[j].v[v]), to_f32(ir[j].v[v]), rate[v]);
-                a[j][v] = k.a;
-                b[j][v] = k.m * k.si * to_f32(xr[j].v[v]);
-            }
-        }
-        if (PACKED) {
-            const int s = marks.first[w * L + j];
-            if (s >= 0 && in)
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    b[j][v] = fmaf(a[j][v], g.init ? g.init[(long long)s * g.D + c + v] : 0.0f, b[j][v]);
-                    a[j][v] = 0.0f;
-                }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) compose_map<PACKED>(A[v], B[v], a[j][v], b[j][v]);
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) sm.run[w][lane * V + v] = make_float2(A[v], B[v]);
+    if (threadIdx.x < kStages) sm.slot[threadIdx.x] = atomicAdd(tl.ticket, 1);
     __syncthreads();
-    float h[V];
-    enter_state<V, W, PACKED>(tl, it, g.D, c, live, w, lane, start, sm, g.status, h);
-    if (!live || t0 >= g.T) return;
+    for (int k = 0; k < kStages; ++k) fetch(sm.slot[k], k);
 
-    if (chunk_states && t0 % SSD_GLR_CHUNK == 0) {
-        float e[V];
+    for (int n = 0;; ++n) {
+        const int ticket = sm.slot[n & 3], stage = n % kStages;
+        if (ticket >= total) break;
+        const Item it = item_of(tl, ticket);
+        Exchange &ex = sm.ex[n & 1];
+        const Marks<kTile> &marks = sm.marks[n & 1];
+        int next = 0;
+        if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
+        const int c = it.blk * 64 + 2 * lane, t0 = it.step * kTile + w * kL;    // token in the row
+        const bool live = c < g.D, second = c + 1 < g.D;
+        F2 start = f2(0.0f);
+        if (!PACKED && g.init && live && it.step < kGroup) start = load_f32_pair<PAIR>(g.init + (long long)it.row * g.D + c, second);
+        if constexpr (PACKED)
+            mark_sequences(g, sm.marks[n & 1], it.step * kTile, (long long)it.step * tl.nblk + it.blk,
+                           (long long)tl.ntiles * tl.nblk, true, [&](int s) {
+                               if (!final_states) return;
+                               for (int k = it.blk * 64; k < min((it.blk + 1) * 64, g.D); ++k)
+                                   final_states[(long long)s * g.D + k] = g.init ? g.init[(long long)s * g.D + k] : 0.0f;
+                           });
+        copy_wait<kStages - 1>();
+        __syncwarp();
+
+        const F2 rate = each(load_pair(&sm.A_log[stage][w][2 * lane]), [](float v) { return expf(v); });
+        F2 a[kL], b[kL], A = f2(1.0f), B = f2(0.0f);
 #pragma unroll
-        for (int v = 0; v < V; ++v) e[v] = h[v];
-        if (PACKED) {
-            const int s = marks.first[w * L];
-            if (s >= 0)
-#pragma unroll
-                for (int v = 0; v < V; ++v) e[v] = g.init ? g.init[(long long)s * g.D + c + v] : 0.0f;
+        for (int j = 0; j < kL; ++j) {
+            const Gate2 k = gate2(load_pair(&sm.in[stage][w][0][j][2 * lane]), load_pair(&sm.in[stage][w][1][j][2 * lane]), rate);
+            a[j] = k.a;
+            b[j] = mul(mul(k.m, k.si), load_pair(&sm.in[stage][w][2][j][2 * lane]));
         }
-        store_vec<float, V>(chunk_states + ((long long)it.row * g.nchunk + t0 / SSD_GLR_CHUNK) * g.D + c, e);
-    }
+        if (t0 + kL > g.T) {                        // behind the row's end: the state stays
 #pragma unroll
-    for (int j = 0; j < L; ++j)
-        if (t0 + j < g.T) {
+            for (int j = 0; j < kL; ++j)
+                if (t0 + j >= g.T) a[j] = f2(1.0f), b[j] = f2(0.0f);
+        }
+        if constexpr (PACKED) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) h[v] = apply_map<PACKED>(a[j][v], b[j][v], h[v]);
-            if (y) store_vec<T, V>(y + (row0 + t0 + j) * g.D + c, h);
-            if (final_states) {
-                const int s = PACKED ? marks.last[w * L + j] : (t0 + j == g.T - 1 ? it.row : -1);
-                if (s >= 0) store_vec<float, V>(final_states + (long long)s * g.D + c, h);
+            for (int j = 0; j < kL; ++j) {
+                const int s = marks.first[w * kL + j];
+                if (s >= 0) {
+                    if (g.init && live) b[j] = fma(a[j], load_f32_pair<PAIR>(g.init + (long long)s * g.D + c, second), b[j]);
+                    a[j] = f2(0.0f);
+                }
             }
         }
+#pragma unroll
+        for (int j = 0; j < kL; ++j) compose_map<PACKED>(A, B, a[j], b[j]);
+        ex.run[w][lane] = pack_map(A, B);
+        if (threadIdx.x == 0) sm.slot[(n + 2) & 3] = next;
+        __syncthreads();
+        fetch(sm.slot[(n + 2) & 3], stage);
+        F2 h = enter_state<PACKED>(tl, it, w, lane, start, ex, g.status);
+        if (!live || t0 >= g.T) continue;
+
+        if (chunk_states && w == 0) {
+            F2 e = h;
+            if (PACKED && marks.first[0] >= 0)
+                e = g.init ? load_f32_pair<PAIR>(g.init + (long long)marks.first[0] * g.D + c, second) : f2(0.0f);
+            store_pair<PAIR>(chunk_states + ((long long)it.row * g.nchunk + it.step) * g.D + c, e, second);
+        }
+        T *out = y + ((long long)it.row * g.T + t0) * g.D + c;
+#pragma unroll
+        for (int j = 0; j < kL; ++j) {
+            if (t0 + j >= g.T) break;
+            h = apply_map<PACKED>(a[j], b[j], h);
+            if (y) store_pair<PAIR>(out + (long long)j * g.D, h, second);
+            if (final_states) {
+                const int s = PACKED ? marks.last[w * kL + j] : (t0 + j == g.T - 1 ? it.row : -1);
+                if (s >= 0) store_pair<PAIR>(final_states + (long long)s * g.D + c, h, second);
+            }
+        }
+    }
+    copy_wait<0>();
 }
 
 // One tile of L W = SSD_GLR_CHUNK tokens, the row's last tile first.  The
@@ -569,7 +703,7 @@ GlrArgs args_of(const ssd_glr_params &p, const void *x, const void *r, const voi
 }
 
 // Tile shapes: tokens a tile; channels a block is 32 V, V = 1 or 2.
-constexpr int kFwdL = 16, kFwdW = 8, kBwdL = 4, kBwdW = 16;
+constexpr int kBwdL = 4, kBwdW = 16;
 
 // Workspace of one scan: status word, counters and flags (cleared together),
 // then maps and states.  Sized for V = 1, the most channel blocks.
@@ -598,10 +732,12 @@ Scan scan_of(const ssd_glr_params &p, int tile_tokens, int V, bool bwd, char *ws
     s.clear = off;
     off = align_up(off);
     if (t.ntiles > 1) {
-        t.maps = reinterpret_cast<float2 *>(ws + off);
-        off = align_up(off + (size_t)t.rows * t.ntiles * p.channels * sizeof(float2));
-        t.states = reinterpret_cast<float *>(ws + off);
-        off = align_up(off + groups * p.channels * sizeof(float));
+        t.maps = reinterpret_cast<float4 *>(ws + off);
+        t.maps1 = reinterpret_cast<float2 *>(ws + off);
+        off = align_up(off + items * 32 * sizeof(float4));
+        t.states = reinterpret_cast<float2 *>(ws + off);
+        t.states1 = reinterpret_cast<float *>(ws + off);
+        off = align_up(off + groups * t.nblk * 32 * sizeof(float2));
     }
     s.bytes = off;
     return s;
@@ -618,7 +754,7 @@ BwdLayout bwd_layout(const ssd_glr_params &p, bool with_chunks)
     l.part = scan_of(p, kBwdL * kBwdW, 1, true, nullptr).bytes;
     l.chunks = align_up(l.part + n);
     l.total = with_chunks ? l.chunks : align_up(l.chunks + n);
-    const size_t f = scan_of(p, kFwdL * kFwdW, 1, false, nullptr).bytes;
+    const size_t f = scan_of(p, kTile, 2, false, nullptr).bytes;
     if (!with_chunks && f > l.chunks) {          // the forward's scan runs first, in the same place
         l.chunks = f;
         l.total = align_up(f + n);
@@ -638,14 +774,57 @@ int width_of(const ssd_glr_params &p, std::initializer_list<const void *> io, st
     return 2;
 }
 
-template <typename T, int V>
-void launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+int sm_count()
 {
-    const unsigned grid = (unsigned)((size_t)tl.rows * tl.ntiles * tl.nblk);
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Bytes of one copy that the rows allow: 16, two elements or one.
+int copy_bytes(const ssd_glr_params &p, std::initializer_list<const void *> io, std::initializer_list<const void *> f32)
+{
+    const int es = (int)elem_size(p.io_dtype);
+    for (const int n : {16, 2 * es}) {
+        const int per = n / es;
+        bool ok = p.channels % per == 0 && p.x_stride % per == 0 && p.r_stride % per == 0 && p.i_stride % per == 0;
+        for (const void *q : io) ok = ok && aligned(q, n);
+        for (const void *q : f32) ok = ok && aligned(q, 8);
+        if (ok) return n;
+    }
+    return es;
+}
+
+template <typename T, int COPY, bool PACKED>
+cudaError_t launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+{
+    const auto kernel = glr_fwd_kernel<T, COPY, PACKED>;
+    const int smem = sizeof(FwdSmem<T>);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long items = (long long)tl.rows * tl.ntiles * tl.nblk;
+    const int grid = (int)std::min<long long>(items, (long long)sm_count() * (sizeof(T) == 2 ? 3 : 2));
+    kernel<<<grid, 32 * kW, smem, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+    return cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_fwd(const GlrArgs &g, int copy, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+{
+    constexpr int P = 2 * sizeof(T), S = sizeof(T);
     if (g.cu)
-        glr_fwd_kernel<T, V, kFwdL, kFwdW, true><<<grid, 32 * kFwdW, 0, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
-    else
-        glr_fwd_kernel<T, V, kFwdL, kFwdW, false><<<grid, 32 * kFwdW, 0, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+        return copy == 16  ? launch_fwd<T, 16, true>(g, tl, y, fin, chunks, st)
+               : copy == P ? launch_fwd<T, P, true>(g, tl, y, fin, chunks, st)
+                           : launch_fwd<T, S, true>(g, tl, y, fin, chunks, st);
+    return copy == 16  ? launch_fwd<T, 16, false>(g, tl, y, fin, chunks, st)
+           : copy == P ? launch_fwd<T, P, false>(g, tl, y, fin, chunks, st)
+                       : launch_fwd<T, S, false>(g, tl, y, fin, chunks, st);
 }
 
 cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_t st)
@@ -659,17 +838,13 @@ cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_
 cudaError_t run_fwd(const ssd_glr_params &p, const GlrArgs &g, void *y, float *fin, float *chunks, char *ws,
                     cudaStream_t st)
 {
-    const int V = width_of(p, {g.x, g.r, g.i, y}, {fin, chunks});
-    const Scan s = scan_of(p, kFwdL * kFwdW, V, false, ws);
+    const int copy = copy_bytes(p, {g.x, g.r, g.i, y}, {g.init, fin, chunks});
+    const Scan s = scan_of(p, kTile, 2, false, ws);
     const cudaError_t e = cudaMemsetAsync(ws, 0, s.clear, st);
     if (e != cudaSuccess) return e;
     if (p.seqlen == 0) return fin ? run_copy(g, g.init, fin, st) : cudaSuccess;
-    const bool bf = p.io_dtype == SSD_DTYPE_BF16;
-    if (bf && V == 2) launch_fwd<__nv_bfloat16, 2>(g, s.tl, y, fin, chunks, st);
-    else if (bf) launch_fwd<__nv_bfloat16, 1>(g, s.tl, y, fin, chunks, st);
-    else if (V == 2) launch_fwd<float, 2>(g, s.tl, y, fin, chunks, st);
-    else launch_fwd<float, 1>(g, s.tl, y, fin, chunks, st);
-    return cudaGetLastError();
+    return p.io_dtype == SSD_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(g, copy, s.tl, y, fin, chunks, st)
+                                        : launch_fwd<float>(g, copy, s.tl, y, fin, chunks, st);
 }
 
 struct BwdArgs {
@@ -703,7 +878,7 @@ extern "C" {
 
 size_t ssd_glr_fwd_workspace_size(const ssd_glr_params *p)
 {
-    return validate(p) == SSD_OK ? scan_of(*p, kFwdL * kFwdW, 1, false, nullptr).bytes : 0;
+    return validate(p) == SSD_OK ? scan_of(*p, kTile, 2, false, nullptr).bytes : 0;
 }
 
 size_t ssd_glr_bwd_workspace_size(const ssd_glr_params *p, int with_chunk_states)

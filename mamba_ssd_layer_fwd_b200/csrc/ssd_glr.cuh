@@ -87,6 +87,140 @@ __device__ __forceinline__ Gate gate(float r, float i, float rate)
     return g;
 }
 
+// ---------------------------------------------------------------- pairs of channels
+// Two float32 in a register pair: sm_100's paired instructions do two
+// operations for one issue slot, and issue slots are what the scan kernels run
+// out of next after HBM.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y)
+{
+    F2 o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o.v) : "f"(x), "f"(y));
+    return o;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 o;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+    return o;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 o;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+    return o;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 o;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return o;
+}
+template <typename Op>
+__device__ __forceinline__ F2 each(F2 a, Op op)
+{
+    float x, y;
+    split(a, x, y);
+    return f2(op(x), op(y));
+}
+__device__ __forceinline__ F2 shown(float2 a) { return f2(a.x, a.y); }
+
+// Gates of two channels.  Four special-function operations an element: the two
+// sigmoids share one reciprocal (exponents clamped so that the product of the
+// denominators stays below 2^125), and exp(-q) is taken on the FMA units, since
+// the special-function unit (16 lanes a clock and SM) would otherwise bound the
+// kernels.  1 - a^2 = (1 - a)(1 + a) needs 1 - a to full relative precision
+// for small q: q = n ln2 + f (two-term ln2, the usual argument reduction),
+// v = 1 - exp(-f) = f u with u a polynomial (degree 5, fitted on |f| <= 0.3467
+// at Chebyshev nodes, 2.4e-8 of u), s = 2^-n, a = s (1 - v), 1 - a = s v + (1 - s).
+struct Gate2 {
+    F2 a, m, inv_m, q;          // exp(-q), sqrt(1 - a^2), 1 / m (finite at m = 0), exp(A_log) sigmoid(r)
+    F2 si, osi, osr;            // sigmoid(i), sigmoid(-i), sigmoid(-r)
+};
+
+__device__ __forceinline__ Gate2 gate2(F2 r, F2 i, F2 rate)
+{
+    const F2 nlog2e = f2(-1.4426950408889634f), one = f2(1.0f), minus = f2(-1.0f);
+    const auto ex = [](float v) { return ex2_approx(min_nan(v, 62.0f)); };
+    Gate2 g;
+    const F2 er = each(mul(r, nlog2e), ex), ei = each(mul(i, nlog2e), ex);
+    const F2 dr = add(er, one), di = add(ei, one);
+    const F2 inv = each(mul(dr, di), [](float v) { return rcp_approx(v); });
+    const F2 sr = mul(di, inv);
+    g.si = mul(dr, inv);
+    g.osr = mul(er, sr);
+    g.osi = mul(ei, g.si);
+    g.q = each(mul(rate, sr), [](float v) { return min_nan(v, 87.0f); });
+    const F2 k = fma(g.q, f2(1.4426950408889634f), f2(12582912.0f));     // 1.5 * 2^23: low bits are rint(q log2 e)
+    const F2 n = add(k, f2(-12582912.0f));
+    F2 f = fma(n, f2(-0.693359375f), g.q);                               // ln2 = 0.693359375 - 2.12194440e-4
+    f = fma(n, f2(2.12194440e-4f), f);
+    const F2 s = each(k, [](float v) { return __int_as_float(__float_as_int(v) * -(1 << 23) + (127 << 23)); });
+    F2 u = fma(f, f2(-1.39337e-3f), f2(8.36319e-3f));
+    u = fma(u, f, f2(-4.166646e-2f));
+    u = fma(u, f, f2(0.16666577f));
+    u = fma(u, f, f2(-0.5f));
+    u = fma(u, f, one);
+    const F2 v = mul(u, f);
+    g.a = mul(s, fma(v, minus, one));
+    const F2 e = fma(s, v, fma(s, minus, one));
+    const F2 w = fma(e, add(g.a, one), f2(1.17549435e-38f));             // 1 - a^2, kept off 0
+    g.inv_m = each(w, [](float x) { return rsqrt_approx(x); });
+    g.m = mul(w, g.inv_m);
+    return g;
+}
+
+template <typename T> __device__ __forceinline__ F2 load_pair(const T *p);      // p aligned to two elements
+template <> __device__ __forceinline__ F2 load_pair<float>(const float *p) { return shown(*reinterpret_cast<const float2 *>(p)); }
+template <> __device__ __forceinline__ F2 load_pair<__nv_bfloat16>(const __nv_bfloat16 *p)
+{
+    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
+    return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// Stores one or two channels; PAIR: both, at an address aligned to two elements.
+template <bool PAIR, typename T>
+__device__ __forceinline__ void store_pair(T *p, F2 f, bool second)
+{
+    float x, y;
+    split(f, x, y);
+    if constexpr (!PAIR) {
+        p[0] = from_f32<T>(x);
+        if (second) p[1] = from_f32<T>(y);
+    } else if constexpr (sizeof(T) == 4) {
+        *reinterpret_cast<float2 *>(p) = make_float2(x, y);
+    } else {
+        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ F2 load_f32_pair(const float *p, bool second)
+{
+    if constexpr (PAIR) return shown(*reinterpret_cast<const float2 *>(p));
+    return f2(p[0], second ? p[1] : 0.0f);
+}
+
+// ---------------------------------------------------------------- copies global -> shared
+// BYTES = 16, 8 or 4 (both addresses aligned to it); `in` false: zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from, bool in)
+{
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    const int n = in ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(from), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
 // ---------------------------------------------------------------- vectors of V adjacent channels
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {
@@ -143,6 +277,15 @@ __device__ __forceinline__ float apply_map(float A, float B, float h)
     return PACKED && A == 0.0f ? B : v;
 }
 
+template <bool PACKED>
+__device__ __forceinline__ F2 apply_map(F2 A, F2 B, F2 h)
+{
+    if constexpr (!PACKED) return fma(A, h, B);
+    float a0, a1, b0, b1, h0, h1;
+    split(A, a0, a1), split(B, b0, b1), split(h, h0, h1);
+    return f2(apply_map<true>(a0, b0, h0), apply_map<true>(a1, b1, h1));
+}
+
 // (A, B) <- (A2, B2) after (A, B)
 template <bool PACKED>
 __device__ __forceinline__ void compose_map(float &A, float &B, float A2, float B2)
@@ -150,6 +293,21 @@ __device__ __forceinline__ void compose_map(float &A, float &B, float A2, float 
     const bool cut = PACKED && A2 == 0.0f;
     B = cut ? B2 : fmaf(A2, B, B2);
     A = cut ? 0.0f : A * A2;
+}
+
+template <bool PACKED>
+__device__ __forceinline__ void compose_map(F2 &A, F2 &B, F2 A2, F2 B2)
+{
+    if constexpr (PACKED) {
+        float a0, a1, b0, b1, c0, c1, d0, d1;
+        split(A, a0, a1), split(B, b0, b1), split(A2, c0, c1), split(B2, d0, d1);
+        compose_map<true>(a0, b0, c0, d0);
+        compose_map<true>(a1, b1, c1, d1);
+        A = f2(a0, a1), B = f2(b0, b1);
+    } else {
+        B = fma(A2, B, B2);
+        A = mul(A, A2);
+    }
 }
 
 // ---------------------------------------------------------------- waits between CTAs
