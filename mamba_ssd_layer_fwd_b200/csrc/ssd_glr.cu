@@ -214,12 +214,12 @@ __device__ __forceinline__ int take_ticket(const Tiling &tl, int *slot)
     return *slot;
 }
 
-// ---------------------------------------------------------------- scans over pairs of channels
-// A CTA of W warps walks tiles of L W tokens by 64 channels: warp w has the
-// tile's run w of L tokens, a lane two adjacent channels.
-constexpr int kL = 8, kW = 8, kTile = kL * kW, kStages = 2;
+// ---------------------------------------------------------------- the scan kernels' tiles
+// A CTA of kWarps warps walks tiles of kTile tokens by 64 channels.  A lane has
+// four adjacent channels of a run of kL tokens, half a warp one run.
+constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kStages = 2, kThreads = 32 * kWarps;
+static_assert(kTile == SSD_GLR_CHUNK, "a tile starts at a chunk state");
 
-// Maps as (A, B) of a channel pair.
 __device__ __forceinline__ float4 pack_map(F2 A, F2 B)
 {
     float4 m;
@@ -230,107 +230,135 @@ __device__ __forceinline__ F2 map_A(float4 m) { return f2(m.x, m.y); }
 __device__ __forceinline__ F2 map_B(float4 m) { return f2(m.z, m.w); }
 
 struct Exchange {
-    float4 run[kW][32];             // maps of the runs, in scan order
-    float4 tile[kGroup / 2][32];    // maps of the group's earlier tiles, by pairs
-    float2 state[32];               // state after the group before
+    float4 run[kRuns][32];          // maps of the runs, in scan order, by channel pair
+    float2 state[32];               // state entering the tile
 };
 
-// The exchange between the tiles of a row.  ex.run holds the runs' maps (and a
-// barrier has been passed since); publishes the tile's map (and, for a group's
-// last tile, the state after it) and returns the state entering run w of the
-// scan.  `start` is the state entering the row.
+// The exchange between the tiles of a row, by one warp, a channel pair a lane.
+// ex.run holds the runs' maps.  Publishes the tile's map, builds the state that
+// enters the tile from `start`, the state entering the row, and for a group's
+// last tile publishes the state after it.
 template <bool PACKED>
-__device__ __forceinline__ F2 enter_state(const Tiling &tl, const Item &it, int w, int lane, F2 start, Exchange &ex,
-                                          int *status)
+__device__ __forceinline__ void exchange(const Tiling &tl, const Item &it, int lane, float2 start, Exchange &ex,
+                                         int *status)
 {
     const int in_group = it.step % kGroup, group = it.step / kGroup;
     const long long row_tile = (long long)it.row * tl.ntiles;
-    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup, pair0 = it.blk * 32 + lane, npairs = tl.nblk * 32;
-    if (tl.ntiles > 1) {
-        if (w == 0 && it.step + 1 < tl.ntiles) {
-            F2 A = f2(1.0f), B = f2(0.0f);
+    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup, pair = it.blk * 32 + lane, npairs = tl.nblk * 32;
+    const bool more = it.step + 1 < tl.ntiles;
+    F2 A = f2(1.0f), B = f2(0.0f);
+    if (more) {
 #pragma unroll
-            for (int k = 0; k < kW; ++k) {
-                const float4 m = ex.run[k][lane];
-                compose_map<PACKED>(A, B, map_A(m), map_B(m));
-            }
-            __stcg(&tl.maps[(row_tile + it.step) * npairs + pair0], pack_map(A, B));
+        for (int k = 0; k < kRuns; ++k) {
+            const float4 m = ex.run[k][lane];
+            compose_map<PACKED>(A, B, map_A(m), map_B(m));
+        }
+        if (in_group < kGroup - 1) {                // the last tile's is not read by others
+            __stcg(&tl.maps[(row_tile + it.step) * npairs + pair], pack_map(A, B));
             __threadfence();
             __syncwarp();
             if (lane == 0) st_release(&tl.map_flag[(row_tile + it.step) * tl.nblk + it.blk], 1);
         }
-        if (w * 2 < in_group) {                     // kGroup / 2 = kW pairs
-            static_assert(kGroup / 2 <= kW, "one pair of tiles a warp");
-            const int t0 = group * kGroup + w * 2;
-            const bool two = w * 2 + 1 < in_group;
-            bool ok = wait_flag(&tl.map_flag[(row_tile + t0) * tl.nblk + it.blk], status);
-            if (ok && two) ok = wait_flag(&tl.map_flag[(row_tile + t0 + 1) * tl.nblk + it.blk], status);
-            F2 A = f2(1.0f), B = f2(0.0f);
-            if (ok) {
-                const float4 *m = &tl.maps[(row_tile + t0) * npairs + pair0];
-                const float4 m0 = __ldcg(m), m1 = two ? __ldcg(m + npairs) : make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-                A = map_A(m0), B = map_B(m0);
-                compose_map<PACKED>(A, B, map_A(m1), map_B(m1));
-            }
-            ex.tile[w][lane] = pack_map(A, B);
+    }
+    // lane k waits for the group's tile k, the last lane for the group before
+    bool ok = true;
+    const long long before = (long long)it.row * ngroups + group - 1, t0 = row_tile + group * kGroup;
+    if (lane < in_group)
+        ok = wait_flag(&tl.map_flag[(t0 + lane) * tl.nblk + it.blk], status);
+    else if (lane == 31 && group > 0)
+        ok = wait_flag(&tl.state_flag[before * tl.nblk + it.blk], status);
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();                                   // what each lane acquired is there for all
+    F2 h = shown(start);
+    if (ok) {
+        if (group > 0) h = shown(__ldcg(&tl.states[before * npairs + pair]));
+        const float4 *maps = &tl.maps[t0 * npairs + pair];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            float4 m[kGroup / 2];
+#pragma unroll
+            for (int k = 0; k < kGroup / 2; ++k)
+                if (half * kGroup / 2 + k < in_group) m[k] = __ldcg(maps + (long long)(half * kGroup / 2 + k) * npairs);
+#pragma unroll
+            for (int k = 0; k < kGroup / 2; ++k)
+                if (half * kGroup / 2 + k < in_group) h = apply_map<PACKED>(map_A(m[k]), map_B(m[k]), h);
         }
-        if (w == kW - 1 && group > 0) {
-            const long long at = (long long)it.row * ngroups + group - 1;
-            const bool ok = wait_flag(&tl.state_flag[at * tl.nblk + it.blk], status);
-            ex.state[lane] = ok ? __ldcg(&tl.states[at * npairs + pair0]) : make_float2(0.0f, 0.0f);
-        }
-        __syncthreads();
     }
-    F2 h = group > 0 ? shown(ex.state[lane]) : start;
-    for (int k = 0; k * 2 < in_group; ++k) {
-        const float4 m = ex.tile[k][lane];
-        h = apply_map<PACKED>(map_A(m), map_B(m), h);
-    }
-    for (int k = 0; k < w; ++k) {
-        const float4 m = ex.run[k][lane];
-        h = apply_map<PACKED>(map_A(m), map_B(m), h);
-    }
-    if (w == kW - 1 && in_group == kGroup - 1 && it.step + 1 < tl.ntiles &&
-        *reinterpret_cast<volatile int *>(status) != kDevTimeout) {
-        const long long at = (long long)it.row * ngroups + group;
-        const float4 m = ex.run[w][lane];
-        float2 o;
-        split(apply_map<PACKED>(map_A(m), map_B(m), h), o.x, o.y);
-        __stcg(&tl.states[at * npairs + pair0], o);
+    float2 o;
+    split(h, o.x, o.y);
+    ex.state[lane] = o;
+    if (ok && more && in_group == kGroup - 1) {
+        split(apply_map<PACKED>(A, B, h), o.x, o.y);
+        __stcg(&tl.states[(before + 1) * npairs + pair], o);
         __threadfence();
         __syncwarp();
-        if (lane == 0) st_release(&tl.state_flag[at * tl.nblk + it.blk], 1);
+        if (lane == 0) st_release(&tl.state_flag[(before + 1) * tl.nblk + it.blk], 1);
+    }
+}
+
+// The state that enters run `run` of the tile, of the lane's two channel pairs.
+template <bool PACKED>
+__device__ __forceinline__ F4 enter_run(const Exchange &ex, int run, int quad)
+{
+    const float4 v = *reinterpret_cast<const float4 *>(&ex.state[2 * quad]);
+    F4 h = {f2(v.x, v.y), f2(v.z, v.w)};
+    for (int k = 0; k < run; ++k) {
+        const float4 m0 = ex.run[k][2 * quad], m1 = ex.run[k][2 * quad + 1];
+        h.p[0] = apply_map<PACKED>(map_A(m0), map_B(m0), h.p[0]);
+        h.p[1] = apply_map<PACKED>(map_A(m1), map_B(m1), h.p[1]);
     }
     return h;
 }
 
-// Copies a run's tokens [t0, t0 + kL) of one array, channels c0 .. c0 + 63, to
-// dst[kL][64]; zeros outside the row or the channels.  COPY is what the rows'
+// Copies tokens [t0, t0 + 2 kL) of one array, channels c0 .. c0 + 63, to
+// dst[2 kL][64]; zeros outside the row or the channels.  COPY is what the rows'
 // alignment allows: 16 bytes, two elements, or one.  A warp's work.
 template <typename T, int COPY>
-__device__ __forceinline__ void stage_run(T *dst, const T *src, long long stride, int t0, int T_, int c0, int D, int lane)
+__device__ __forceinline__ void stage_runs(T *dst, const T *row, long long stride, int t0, int T_, int c0, int D, int lane)
 {
     constexpr int N = COPY / sizeof(T);             // channels of a copy
     constexpr int PER = 64 / N;                     // copies of a token
+    constexpr int STEP = PER < 32 ? 32 / PER : 1;   // tokens a warp copies at once
+    constexpr int COLS = PER > 32 ? PER / 32 : 1;
+    const int c = (lane % PER) * N, r0 = lane / PER;
+    const T *from = row + (long long)(t0 + r0) * stride + c0 + c;
 #pragma unroll
-    for (int k = 0; k < kL * PER / 32; ++k) {
-        const int id = k * 32 + lane, row = id / PER, c = id % PER * N;
-        const bool in = t0 + row < T_ && c0 + c < D;
-        const T *from = in ? src + (long long)(t0 + row) * stride + c0 + c : src;
-        if constexpr (COPY >= 4)
-            copy_async<COPY>(dst + row * 64 + c, from, in);
-        else
-            dst[row * 64 + c] = in ? *from : from_f32<T>(0.0f);
-    }
+    for (int k = 0; k < 2 * kL / STEP; ++k, from += STEP * stride)
+#pragma unroll
+        for (int q = 0; q < COLS; ++q) {
+            const bool in = t0 + r0 + k * STEP < T_ && c0 + c + q * 32 * N < D;
+            T *to = dst + (r0 + k * STEP) * 64 + c + q * 32 * N;
+            if constexpr (COPY >= 4)
+                copy_async<COPY>(to, in ? from + q * 32 * N : row, in);
+            else
+                *to = in ? from[q * 32 * N] : from_f32<T>(0.0f);
+        }
+}
+
+// A run's marks as bits: token j of the run starts (ends) a sequence.
+struct RunMarks {
+    unsigned first, last;
+};
+__device__ __forceinline__ RunMarks run_marks(const Marks<kTile> &m, int run, int lane)
+{
+    const int j = lane % kL, at = run * kL + j;
+    const unsigned f = __ballot_sync(0xffffffffu, m.first[at] >= 0), l = __ballot_sync(0xffffffffu, m.last[at] >= 0);
+    const int shift = lane & 16;                    // the half warp's own run
+    return {(f >> shift) & 0xffu, (l >> shift) & 0xffu};
 }
 
 template <typename T> struct FwdSmem {
-    T in[kStages][kW][3][kL][64];   // r, i, x
-    float A_log[kStages][kW][64];
-    Exchange ex[2];
-    Marks<kTile> marks[2];
-    int slot[4];
+    T in[kStages][kWarps][3][2 * kL][64];   // r, i, x
+    Exchange ex;
+    int4 slot[4];                   // row, step, block of the next tiles; w: 0 when there are none
 };
+
+__device__ __forceinline__ int4 draw_item(const Tiling &tl, int total)
+{
+    const int ticket = atomicAdd(tl.ticket, 1);
+    const Item it = item_of(tl, ticket);
+    return make_int4(it.row, it.step, it.blk, ticket < total);
+}
 
 // y (NULL: chunk states only), final_states and chunk_states may be NULL.
 //
@@ -339,103 +367,142 @@ template <typename T> struct FwdSmem {
 // waits for other tiles; the ticket of the tile after next is drawn while this
 // one is computed.
 template <typename T, int COPY, bool PACKED>
-__global__ void __launch_bounds__(32 * kW, sizeof(T) == 2 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
 glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ final_states,
                float *__restrict__ chunk_states)
 {
     extern __shared__ __align__(16) char smem_raw[];
     FwdSmem<T> &sm = *reinterpret_cast<FwdSmem<T> *>(smem_raw);
-    constexpr bool PAIR = COPY > sizeof(T);
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    __shared__ Marks<PACKED ? kTile : 1> marks;
+    constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int total = tl.rows * tl.ntiles * tl.nblk;
 
-    const auto fetch = [&](int ticket, int stage) {
-        if (ticket < total) {
-            const Item it = item_of(tl, ticket);
-            const int t0 = it.step * kTile + w * kL, c0 = it.blk * 64, c = c0 + 2 * lane;
-            const long long row0 = (long long)it.row * g.T;
-            stage_run<T, COPY>(sm.in[stage][w][0][0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
-            stage_run<T, COPY>(sm.in[stage][w][1][0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
-            stage_run<T, COPY>(sm.in[stage][w][2][0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
-            copy_async<4>(&sm.A_log[stage][w][2 * lane], g.A_log + min(c, g.D - 1), c < g.D);
-            copy_async<4>(&sm.A_log[stage][w][2 * lane + 1], g.A_log + min(c + 1, g.D - 1), c + 1 < g.D);
+    const auto fetch = [&](int4 it, int stage) {
+        if (it.w) {
+            const int t0 = it.y * kTile + w * 2 * kL, c0 = it.z * 64;
+            const long long row0 = (long long)it.x * g.T;
+            T(*in)[2 * kL][64] = sm.in[stage][w];
+            stage_runs<T, COPY>(in[0][0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
+            stage_runs<T, COPY>(in[1][0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
+            stage_runs<T, COPY>(in[2][0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
         }
         copy_commit();
     };
 
-    if (threadIdx.x < kStages) sm.slot[threadIdx.x] = atomicAdd(tl.ticket, 1);
+    if (threadIdx.x == 0)
+        for (int k = 0; k < kStages; ++k) sm.slot[k] = draw_item(tl, total);
     __syncthreads();
     for (int k = 0; k < kStages; ++k) fetch(sm.slot[k], k);
 
     for (int n = 0;; ++n) {
-        const int ticket = sm.slot[n & 3], stage = n % kStages;
-        if (ticket >= total) break;
-        const Item it = item_of(tl, ticket);
-        Exchange &ex = sm.ex[n & 1];
-        const Marks<kTile> &marks = sm.marks[n & 1];
-        int next = 0;
-        if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
-        const int c = it.blk * 64 + 2 * lane, t0 = it.step * kTile + w * kL;    // token in the row
-        const bool live = c < g.D, second = c + 1 < g.D;
-        F2 start = f2(0.0f);
-        if (!PACKED && g.init && live && it.step < kGroup) start = load_f32_pair<PAIR>(g.init + (long long)it.row * g.D + c, second);
-        if constexpr (PACKED)
-            mark_sequences(g, sm.marks[n & 1], it.step * kTile, (long long)it.step * tl.nblk + it.blk,
+        const int4 s4 = sm.slot[n & 3];
+        if (!s4.w) break;
+        const Item it{s4.x, s4.y, s4.z};
+        const int stage = n % kStages;
+        int4 next = make_int4(0, 0, 0, 0);
+        if (threadIdx.x == 0) next = draw_item(tl, total);
+        const int c = it.blk * 64 + 4 * quad, t0 = it.step * kTile + run * kL, nc = g.D - c;
+        const bool live = nc > 0;
+        F4 rate = {f2(0.0f), f2(0.0f)};
+        if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
+        copy_wait<kStages - 1>();
+        __syncthreads();                            // every warp is done with the tile before
+        RunMarks rm{0, 0};
+        if constexpr (PACKED) {
+            mark_sequences(g, marks, it.step * kTile, (long long)it.step * tl.nblk + it.blk,
                            (long long)tl.ntiles * tl.nblk, true, [&](int s) {
                                if (!final_states) return;
                                for (int k = it.blk * 64; k < min((it.blk + 1) * 64, g.D); ++k)
                                    final_states[(long long)s * g.D + k] = g.init ? g.init[(long long)s * g.D + k] : 0.0f;
                            });
-        copy_wait<kStages - 1>();
-        __syncwarp();
+            rm = run_marks(marks, run, lane);
+        }
+        const auto ex = [](float v) { return expf(v); };
+        rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
 
-        const F2 rate = each(load_pair(&sm.A_log[stage][w][2 * lane]), [](float v) { return expf(v); });
-        F2 a[kL], b[kL], A = f2(1.0f), B = f2(0.0f);
+        F4 a[kL], b[kL];
+        T(*in)[2 * kL][64] = sm.in[stage][w];
 #pragma unroll
         for (int j = 0; j < kL; ++j) {
-            const Gate2 k = gate2(load_pair(&sm.in[stage][w][0][j][2 * lane]), load_pair(&sm.in[stage][w][1][j][2 * lane]), rate);
-            a[j] = k.a;
-            b[j] = mul(mul(k.m, k.si), load_pair(&sm.in[stage][w][2][j][2 * lane]));
+            const int row = half * kL + j;
+            const F4 r4 = load4(&in[0][row][4 * quad]), i4 = load4(&in[1][row][4 * quad]), x4 = load4(&in[2][row][4 * quad]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const Gate2 k = gate2(r4.p[p], i4.p[p], rate.p[p]);
+                a[j].p[p] = k.a;
+                b[j].p[p] = mul(mul(k.m, k.si), x4.p[p]);
+            }
         }
         if (t0 + kL > g.T) {                        // behind the row's end: the state stays
 #pragma unroll
             for (int j = 0; j < kL; ++j)
-                if (t0 + j >= g.T) a[j] = f2(1.0f), b[j] = f2(0.0f);
-        }
-        if constexpr (PACKED) {
+                if (t0 + j >= g.T)
 #pragma unroll
-            for (int j = 0; j < kL; ++j) {
-                const int s = marks.first[w * kL + j];
-                if (s >= 0) {
-                    if (g.init && live) b[j] = fma(a[j], load_f32_pair<PAIR>(g.init + (long long)s * g.D + c, second), b[j]);
-                    a[j] = f2(0.0f);
+                    for (int p = 0; p < 2; ++p) a[j].p[p] = f2(1.0f), b[j].p[p] = f2(0.0f);
+        }
+        if (PACKED && rm.first) {
+#pragma unroll
+            for (int j = 0; j < kL; ++j)
+                if (rm.first >> j & 1) {
+                    F4 h0 = {f2(0.0f), f2(0.0f)};
+                    if (g.init && live) h0 = load4_global<ALIGN>(g.init + (long long)marks.first[run * kL + j] * g.D + c, nc);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) b[j].p[p] = fma(a[j].p[p], h0.p[p], b[j].p[p]), a[j].p[p] = f2(0.0f);
                 }
-            }
         }
 #pragma unroll
-        for (int j = 0; j < kL; ++j) compose_map<PACKED>(A, B, a[j], b[j]);
-        ex.run[w][lane] = pack_map(A, B);
+        for (int p = 0; p < 2; ++p) {
+            F2 A = a[0].p[p], B = b[0].p[p];
+#pragma unroll
+            for (int j = 1; j < kL; ++j) compose_map<PACKED>(A, B, a[j].p[p], b[j].p[p]);
+            sm.ex.run[run][2 * quad + p] = pack_map(A, B);
+        }
         if (threadIdx.x == 0) sm.slot[(n + 2) & 3] = next;
         __syncthreads();
         fetch(sm.slot[(n + 2) & 3], stage);
-        F2 h = enter_state<PACKED>(tl, it, w, lane, start, ex, g.status);
+        if (w == 0) {
+            float2 start = make_float2(0.0f, 0.0f);
+            const int cp = it.blk * 64 + 2 * lane;
+            if (!PACKED && g.init && it.step < kGroup && cp < g.D)
+                start = make_float2(g.init[(long long)it.row * g.D + cp],
+                                    cp + 1 < g.D ? g.init[(long long)it.row * g.D + cp + 1] : 0.0f);
+            if (tl.ntiles > 1)
+                exchange<PACKED>(tl, it, lane, start, sm.ex, g.status);
+            else
+                sm.ex.state[lane] = start;
+        }
+        __syncthreads();
+        F4 h = enter_run<PACKED>(sm.ex, run, quad);
         if (!live || t0 >= g.T) continue;
 
-        if (chunk_states && w == 0) {
-            F2 e = h;
-            if (PACKED && marks.first[0] >= 0)
-                e = g.init ? load_f32_pair<PAIR>(g.init + (long long)marks.first[0] * g.D + c, second) : f2(0.0f);
-            store_pair<PAIR>(chunk_states + ((long long)it.row * g.nchunk + it.step) * g.D + c, e, second);
+        if (chunk_states && run == 0) {
+            F4 e = h;
+            if (PACKED && (rm.first & 1)) {
+                e = {f2(0.0f), f2(0.0f)};
+                if (g.init) e = load4_global<ALIGN>(g.init + (long long)marks.first[0] * g.D + c, nc);
+            }
+            store4<ALIGN>(chunk_states + ((long long)it.row * g.nchunk + it.step) * g.D + c, e, nc);
         }
+        if (!y) continue;
         T *out = y + ((long long)it.row * g.T + t0) * g.D + c;
+        const bool ends = PACKED ? rm.last != 0 : t0 + kL >= g.T;     // a last token, or tokens behind the row
+        if (!ends && (!PACKED || t0 + kL <= g.T)) {
 #pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            if (t0 + j >= g.T) break;
-            h = apply_map<PACKED>(a[j], b[j], h);
-            if (y) store_pair<PAIR>(out + (long long)j * g.D, h, second);
-            if (final_states) {
-                const int s = PACKED ? marks.last[w * kL + j] : (t0 + j == g.T - 1 ? it.row : -1);
-                if (s >= 0) store_pair<PAIR>(final_states + (long long)s * g.D + c, h, second);
+            for (int j = 0; j < kL; ++j, out += g.D) {
+#pragma unroll
+                for (int p = 0; p < 2; ++p) h.p[p] = apply_map<PACKED>(a[j].p[p], b[j].p[p], h.p[p]);
+                store4<ALIGN>(out, h, nc);
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < kL; ++j, out += g.D) {
+                if (t0 + j >= g.T) break;
+#pragma unroll
+                for (int p = 0; p < 2; ++p) h.p[p] = apply_map<PACKED>(a[j].p[p], b[j].p[p], h.p[p]);
+                store4<ALIGN>(out, h, nc);
+                const int s = PACKED ? marks.last[run * kL + j] : (t0 + j == g.T - 1 ? it.row : -1);
+                if (final_states && s >= 0) store4<ALIGN>(final_states + (long long)s * g.D + c, h, nc);
             }
         }
     }
@@ -795,7 +862,7 @@ int copy_bytes(const ssd_glr_params &p, std::initializer_list<const void *> io, 
         const int per = n / es;
         bool ok = p.channels % per == 0 && p.x_stride % per == 0 && p.r_stride % per == 0 && p.i_stride % per == 0;
         for (const void *q : io) ok = ok && aligned(q, n);
-        for (const void *q : f32) ok = ok && aligned(q, 8);
+        for (const void *q : f32) ok = ok && aligned(q, n == 16 ? 16 : 8);
         if (ok) return n;
     }
     return es;
@@ -809,8 +876,8 @@ cudaError_t launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, 
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long items = (long long)tl.rows * tl.ntiles * tl.nblk;
-    const int grid = (int)std::min<long long>(items, (long long)sm_count() * (sizeof(T) == 2 ? 3 : 2));
-    kernel<<<grid, 32 * kW, smem, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+    const int grid = (int)std::min<long long>(items, (long long)sm_count() * (sizeof(T) == 2 ? 4 : 2));
+    kernel<<<grid, kThreads, smem, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
     return cudaGetLastError();
 }
 
@@ -838,7 +905,7 @@ cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_
 cudaError_t run_fwd(const ssd_glr_params &p, const GlrArgs &g, void *y, float *fin, float *chunks, char *ws,
                     cudaStream_t st)
 {
-    const int copy = copy_bytes(p, {g.x, g.r, g.i, y}, {g.init, fin, chunks});
+    const int copy = copy_bytes(p, {g.x, g.r, g.i, y}, {g.A_log, g.init, fin, chunks});
     const Scan s = scan_of(p, kTile, 2, false, ws);
     const cudaError_t e = cudaMemsetAsync(ws, 0, s.clear, st);
     if (e != cudaSuccess) return e;

@@ -174,35 +174,71 @@ __device__ __forceinline__ Gate2 gate2(F2 r, F2 i, F2 rate)
     return g;
 }
 
-template <typename T> __device__ __forceinline__ F2 load_pair(const T *p);      // p aligned to two elements
-template <> __device__ __forceinline__ F2 load_pair<float>(const float *p) { return shown(*reinterpret_cast<const float2 *>(p)); }
-template <> __device__ __forceinline__ F2 load_pair<__nv_bfloat16>(const __nv_bfloat16 *p)
+// Four adjacent channels, as two pairs.  ALIGN is the elements that the
+// address is aligned to (4, 2 or 1) and, where it is 1 or 2, `n` the channels
+// that exist.
+struct F4 {
+    F2 p[2];
+};
+
+__device__ __forceinline__ F4 load4(const float *p)         // 16-byte aligned
 {
-    const uint32_t u = *reinterpret_cast<const uint32_t *>(p);
-    return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+    const float4 v = *reinterpret_cast<const float4 *>(p);
+    return {f2(v.x, v.y), f2(v.z, v.w)};
+}
+__device__ __forceinline__ F4 load4(const __nv_bfloat16 *p) // 8-byte aligned
+{
+    const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return {f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
+            f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))};
 }
 
-// Stores one or two channels; PAIR: both, at an address aligned to two elements.
-template <bool PAIR, typename T>
-__device__ __forceinline__ void store_pair(T *p, F2 f, bool second)
+template <int ALIGN>
+__device__ __forceinline__ F4 load4_global(const float *p, int n)
+{
+    if constexpr (ALIGN == 4) return load4(p);
+    if constexpr (ALIGN == 2) {
+        const float2 a = *reinterpret_cast<const float2 *>(p);
+        const float2 b = n > 2 ? *reinterpret_cast<const float2 *>(p + 2) : make_float2(0.0f, 0.0f);
+        return {f2(a.x, a.y), f2(b.x, b.y)};
+    }
+    return {f2(p[0], n > 1 ? p[1] : 0.0f), f2(n > 2 ? p[2] : 0.0f, n > 3 ? p[3] : 0.0f)};
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(F2 a)
 {
     float x, y;
-    split(f, x, y);
-    if constexpr (!PAIR) {
-        p[0] = from_f32<T>(x);
-        if (second) p[1] = from_f32<T>(y);
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float2 *>(p) = make_float2(x, y);
-    } else {
-        *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
-    }
+    split(a, x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <bool PAIR>
-__device__ __forceinline__ F2 load_f32_pair(const float *p, bool second)
+template <int ALIGN, typename T>
+__device__ __forceinline__ void store4(T *p, const F4 &f, int n)
 {
-    if constexpr (PAIR) return shown(*reinterpret_cast<const float2 *>(p));
-    return f2(p[0], second ? p[1] : 0.0f);
+    if constexpr (ALIGN == 1) {
+        float v[4];
+        split(f.p[0], v[0], v[1]), split(f.p[1], v[2], v[3]);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < n) p[k] = from_f32<T>(v[k]);
+    } else if constexpr (sizeof(T) == 2) {
+        if constexpr (ALIGN == 4) {
+            *reinterpret_cast<uint2 *>(p) = make_uint2(pack_bf16(f.p[0]), pack_bf16(f.p[1]));
+        } else {
+            *reinterpret_cast<uint32_t *>(p) = pack_bf16(f.p[0]);
+            if (n > 2) *reinterpret_cast<uint32_t *>(p + 2) = pack_bf16(f.p[1]);
+        }
+    } else {
+        float4 v;
+        split(f.p[0], v.x, v.y), split(f.p[1], v.z, v.w);
+        if constexpr (ALIGN == 4) {
+            *reinterpret_cast<float4 *>(p) = v;
+        } else {
+            *reinterpret_cast<float2 *>(p) = make_float2(v.x, v.y);
+            if (n > 2) *reinterpret_cast<float2 *>(p + 2) = make_float2(v.z, v.w);
+        }
+    }
 }
 
 // ---------------------------------------------------------------- copies global -> shared
