@@ -253,46 +253,45 @@ __device__ __forceinline__ void exchange(const Tiling &tl, const Item &it, int l
             const float4 m = ex.run[k][lane];
             compose_map<PACKED>(A, B, map_A(m), map_B(m));
         }
-        if (in_group < kGroup - 1) {                // the last tile's is not read by others
-            __stcg(&tl.maps[(row_tile + it.step) * npairs + pair], pack_map(A, B));
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) st_release(&tl.map_flag[(row_tile + it.step) * tl.nblk + it.blk], 1);
-        }
+        if (in_group < kGroup - 1)                  // the last tile's is not read by others
+            post(&tl.maps[(row_tile + it.step) * npairs + pair], pack_map(A, B));
     }
-    // lane k waits for the group's tile k, the last lane for the group before
-    bool ok = true;
-    const long long before = (long long)it.row * ngroups + group - 1, t0 = row_tile + group * kGroup;
-    if (lane < in_group)
-        ok = wait_flag(&tl.map_flag[(t0 + lane) * tl.nblk + it.blk], status);
-    else if (lane == 31 && group > 0)
-        ok = wait_flag(&tl.state_flag[before * tl.nblk + it.blk], status);
-    ok = __all_sync(0xffffffffu, ok);
-    __syncwarp();                                   // what each lane acquired is there for all
     F2 h = shown(start);
-    if (ok) {
-        if (group > 0) h = shown(__ldcg(&tl.states[before * npairs + pair]));
-        const float4 *maps = &tl.maps[t0 * npairs + pair];
+    Patience wait;
+    bool ok = true;
+    const long long before = (long long)it.row * ngroups + group - 1;
+    if (group > 0) {
+        uint2 v;
+        while (!written(v = peek(&tl.states[before * npairs + pair])) && (ok = wait.more(status))) {}
+        h = shown(value_of(v));
+    }
+    const float4 *maps = &tl.maps[(row_tile + group * kGroup) * npairs + pair];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            float4 m[kGroup / 2];
+    for (int part = 0; part < kGroup; part += kGroup / 2) {
+        uint4 m[kGroup / 2];
+        bool all;
+        do {
+            all = true;
 #pragma unroll
             for (int k = 0; k < kGroup / 2; ++k)
-                if (half * kGroup / 2 + k < in_group) m[k] = __ldcg(maps + (long long)(half * kGroup / 2 + k) * npairs);
+                if (part + k < in_group) m[k] = peek(maps + (long long)(part + k) * npairs);
 #pragma unroll
             for (int k = 0; k < kGroup / 2; ++k)
-                if (half * kGroup / 2 + k < in_group) h = apply_map<PACKED>(map_A(m[k]), map_B(m[k]), h);
-        }
+                if (part + k < in_group) all = all && written(m[k]);
+        } while (!all && (ok = ok && wait.more(status)));
+#pragma unroll
+        for (int k = 0; k < kGroup / 2; ++k)
+            if (part + k < in_group) {
+                const float4 v = value_of(m[k]);
+                h = apply_map<PACKED>(map_A(v), map_B(v), h);
+            }
     }
     float2 o;
     split(h, o.x, o.y);
     ex.state[lane] = o;
     if (ok && more && in_group == kGroup - 1) {
         split(apply_map<PACKED>(A, B, h), o.x, o.y);
-        __stcg(&tl.states[(before + 1) * npairs + pair], o);
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) st_release(&tl.state_flag[(before + 1) * tl.nblk + it.blk], 1);
+        post(&tl.states[(before + 1) * npairs + pair], o);
     }
 }
 
@@ -460,7 +459,7 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         }
         if (threadIdx.x == 0) sm.slot[(n + 2) & 3] = next;
         __syncthreads();
-        fetch(sm.slot[(n + 2) & 3], stage);
+        if (w != 0) fetch(sm.slot[(n + 2) & 3], stage);
         if (w == 0) {
             float2 start = make_float2(0.0f, 0.0f);
             const int cp = it.blk * 64 + 2 * lane;
@@ -473,6 +472,7 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
                 sm.ex.state[lane] = start;
         }
         __syncthreads();
+        if (w == 0) fetch(sm.slot[(n + 2) & 3], stage);
         F4 h = enter_run<PACKED>(sm.ex, run, quad);
         if (!live || t0 >= g.T) continue;
 
@@ -796,7 +796,6 @@ Scan scan_of(const ssd_glr_params &p, int tile_tokens, int V, bool bwd, char *ws
         t.map_flag = take(items);
         t.state_flag = take(groups * t.nblk);
     }
-    s.clear = off;
     off = align_up(off);
     if (t.ntiles > 1) {
         t.maps = reinterpret_cast<float4 *>(ws + off);
@@ -806,6 +805,7 @@ Scan scan_of(const ssd_glr_params &p, int tile_tokens, int V, bool bwd, char *ws
         t.states1 = reinterpret_cast<float *>(ws + off);
         off = align_up(off + groups * t.nblk * 32 * sizeof(float2));
     }
+    s.clear = off;
     s.bytes = off;
     return s;
 }

@@ -364,6 +364,63 @@ __device__ __forceinline__ uint64_t now_ns()
     return t;
 }
 
+// Values that one CTA hands to others carry their own "written" mark: memory
+// starts at zero, values are stored with their bits inverted, and no value is
+// stored as zero (it would be the NaN of all ones; NaNs are stored as the
+// arithmetic's own, 0x7fffffff).  So a reader polls the values themselves, every
+// 32-bit word on its own, with no flag and no fence between data and flag.
+__device__ __forceinline__ uint32_t to_shared_word(float v) { return ~(v == v ? __float_as_uint(v) : 0x7fffffffu); }
+__device__ __forceinline__ float from_shared_word(uint32_t w) { return __uint_as_float(~w); }
+
+__device__ __forceinline__ void post(float4 *p, float4 v)
+{
+    asm volatile("st.relaxed.gpu.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(to_shared_word(v.x)),
+                 "r"(to_shared_word(v.y)), "r"(to_shared_word(v.z)), "r"(to_shared_word(v.w))
+                 : "memory");
+}
+__device__ __forceinline__ void post(float2 *p, float2 v)
+{
+    asm volatile("st.relaxed.gpu.global.v2.u32 [%0], {%1, %2};" ::"l"(p), "r"(to_shared_word(v.x)),
+                 "r"(to_shared_word(v.y))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 peek(const float4 *p)
+{
+    uint4 v;
+    asm volatile("ld.relaxed.gpu.global.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 peek(const float2 *p)
+{
+    uint2 v;
+    asm volatile("ld.relaxed.gpu.global.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
+    return v;
+}
+__device__ __forceinline__ bool written(uint4 v) { return v.x && v.y && v.z && v.w; }
+__device__ __forceinline__ bool written(uint2 v) { return v.x && v.y; }
+__device__ __forceinline__ float4 value_of(uint4 v)
+{
+    return make_float4(from_shared_word(v.x), from_shared_word(v.y), from_shared_word(v.z), from_shared_word(v.w));
+}
+__device__ __forceinline__ float2 value_of(uint2 v) { return make_float2(from_shared_word(v.x), from_shared_word(v.y)); }
+
+// Counts a wait's polls: false once it has lasted 2 s, or another wait of the
+// call has given up; then the timeout is on record.
+struct Patience {
+    uint64_t t0 = 0;
+    uint32_t polls = 0;
+    __device__ __forceinline__ bool more(int *status)
+    {
+        if (++polls & 63u) return true;
+        if (t0 == 0) t0 = now_ns();
+        if (*reinterpret_cast<volatile int *>(status) == kDevTimeout) return false;
+        if (now_ns() - t0 <= 2000000000ull) return true;
+        atomicExch(status, kDevTimeout);
+        return false;
+    }
+};
+
 // Until *flag is set; after 2 s, or as soon as another wait of the call has
 // given up, records the timeout and returns false.
 __device__ __forceinline__ bool wait_flag(const int *flag, int *status)
