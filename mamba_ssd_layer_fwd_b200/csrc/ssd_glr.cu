@@ -230,83 +230,123 @@ __device__ __forceinline__ F2 map_A(float4 m) { return f2(m.x, m.y); }
 __device__ __forceinline__ F2 map_B(float4 m) { return f2(m.z, m.w); }
 
 struct Exchange {
-    float4 run[kRuns][32];          // maps of the runs, in scan order, by channel pair
-    float2 state[32];               // state entering the tile
+    float4 run[kRuns][32];          // maps of the tile's runs, in scan order, by channel pair
+    float4 tile[kWarps][32];        // maps of the group's earlier tiles, kGroup / kWarps at a time
+    float2 state[32];               // state after the group before (in the first group: entering the row)
 };
 
-// The exchange between the tiles of a row, by one warp, a channel pair a lane.
-// ex.run holds the runs' maps.  Publishes the tile's map, builds the state that
-// enters the tile from `start`, the state entering the row, and for a group's
-// last tile publishes the state after it.
+// A warp's share of the exchange between the tiles of a row, a channel pair a
+// lane: fetches kGroup / kWarps of the group's earlier tiles' maps (one round
+// trip to L2 when they are there) and leaves their composition in ex.tile; the
+// last warp also fetches the state after the group before.
 template <bool PACKED>
-__device__ __forceinline__ void exchange(const Tiling &tl, const Item &it, int lane, float2 start, Exchange &ex,
-                                         int *status)
+__device__ __forceinline__ void gather_maps(const Tiling &tl, const Item &it, int w, int lane, const float *row_start,
+                                            int D, Exchange &ex, int *status)
 {
-    const int in_group = it.step % kGroup, group = it.step / kGroup;
-    const long long row_tile = (long long)it.row * tl.ntiles;
-    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup, pair = it.blk * 32 + lane, npairs = tl.nblk * 32;
-    const bool more = it.step + 1 < tl.ntiles;
-    F2 A = f2(1.0f), B = f2(0.0f);
-    if (more) {
-#pragma unroll
-        for (int k = 0; k < kRuns; ++k) {
-            const float4 m = ex.run[k][lane];
-            compose_map<PACKED>(A, B, map_A(m), map_B(m));
-        }
-        if (in_group < kGroup - 1)                  // the last tile's is not read by others
-            post(&tl.maps[(row_tile + it.step) * npairs + pair], pack_map(A, B));
+    constexpr int N = kGroup / kWarps;
+    const int in_group = it.step % kGroup, group = it.step / kGroup, npairs = tl.nblk * 32, pair = it.blk * 32 + lane;
+    const int cnt = min(max(in_group - w * N, 0), N);
+    const bool state = w == kWarps - 1 && group > 0;
+    if (w == kWarps - 1 && group == 0) {
+        const int c = 2 * pair;
+        ex.state[lane] = make_float2(row_start && c < D ? row_start[c] : 0.0f, row_start && c + 1 < D ? row_start[c + 1] : 0.0f);
     }
-    F2 h = shown(start);
+    if (cnt == 0 && !state) return;
+    const float4 *maps = &tl.maps[((long long)it.row * tl.ntiles + group * kGroup + w * N) * npairs + pair];
+    const float2 *before = &tl.states[((long long)it.row * ((tl.ntiles + kGroup - 1) / kGroup) + group - 1) * npairs + pair];
+    uint4 m[N];
+    uint2 s = make_uint2(1, 1);
     Patience wait;
-    bool ok = true;
-    const long long before = (long long)it.row * ngroups + group - 1;
-    if (group > 0) {
-        uint2 v;
-        while (!written(v = peek(&tl.states[before * npairs + pair])) && (ok = wait.more(status))) {}
-        h = shown(value_of(v));
-    }
-    const float4 *maps = &tl.maps[(row_tile + group * kGroup) * npairs + pair];
+    bool all;
+    do {
+        all = true;
+        if (state) s = peek(before);
 #pragma unroll
-    for (int part = 0; part < kGroup; part += kGroup / 2) {
-        uint4 m[kGroup / 2];
-        bool all;
-        do {
-            all = true;
+        for (int k = 0; k < N; ++k) m[k] = k < cnt ? peek(maps + (long long)k * npairs) : make_uint4(1, 1, 1, 1);
+        all = written(s);
 #pragma unroll
-            for (int k = 0; k < kGroup / 2; ++k)
-                if (part + k < in_group) m[k] = peek(maps + (long long)(part + k) * npairs);
+        for (int k = 0; k < N; ++k) all = all && written(m[k]);
+    } while (!all && wait.more(status));
+    if (cnt) {
+        float4 v = value_of(m[0]);
+        F2 A = map_A(v), B = map_B(v);
 #pragma unroll
-            for (int k = 0; k < kGroup / 2; ++k)
-                if (part + k < in_group) all = all && written(m[k]);
-        } while (!all && (ok = ok && wait.more(status)));
-#pragma unroll
-        for (int k = 0; k < kGroup / 2; ++k)
-            if (part + k < in_group) {
-                const float4 v = value_of(m[k]);
-                h = apply_map<PACKED>(map_A(v), map_B(v), h);
+        for (int k = 1; k < N; ++k)
+            if (k < cnt) {
+                v = value_of(m[k]);
+                compose_map<PACKED>(A, B, map_A(v), map_B(v));
             }
+        ex.tile[w][lane] = pack_map(A, B);
     }
-    float2 o;
-    split(h, o.x, o.y);
-    ex.state[lane] = o;
-    if (ok && more && in_group == kGroup - 1) {
-        split(apply_map<PACKED>(A, B, h), o.x, o.y);
-        post(&tl.states[(before + 1) * npairs + pair], o);
-    }
+    if (state) ex.state[lane] = value_of(s);
 }
 
-// The state that enters run `run` of the tile, of the lane's two channel pairs.
+struct Map4 {
+    F2 A[2], B[2];
+};
+
+// Composition of the maps of the tile's runs before `run`, of a lane's channels.
 template <bool PACKED>
-__device__ __forceinline__ F4 enter_run(const Exchange &ex, int run, int quad)
+__device__ __forceinline__ Map4 runs_before(const Exchange &ex, int run, int quad)
+{
+    Map4 m = {{f2(1.0f), f2(1.0f)}, {f2(0.0f), f2(0.0f)}};
+#pragma unroll
+    for (int k = 0; k < kRuns - 1; ++k)
+        if (k < run)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 v = ex.run[k][2 * quad + p];
+                compose_map<PACKED>(m.A[p], m.B[p], map_A(v), map_B(v));
+            }
+    return m;
+}
+
+// The state that enters the tile, of a lane's channels (after gather_maps and a barrier).
+template <bool PACKED>
+__device__ __forceinline__ F4 enter_tile(const Exchange &ex, int in_group, int quad)
 {
     const float4 v = *reinterpret_cast<const float4 *>(&ex.state[2 * quad]);
     F4 h = {f2(v.x, v.y), f2(v.z, v.w)};
-    for (int k = 0; k < run; ++k) {
-        const float4 m0 = ex.run[k][2 * quad], m1 = ex.run[k][2 * quad + 1];
-        h.p[0] = apply_map<PACKED>(map_A(m0), map_B(m0), h.p[0]);
-        h.p[1] = apply_map<PACKED>(map_A(m1), map_B(m1), h.p[1]);
-    }
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k)
+        if (k * (kGroup / kWarps) < in_group)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const float4 m = ex.tile[k][2 * quad + p];
+                h.p[p] = apply_map<PACKED>(map_A(m), map_B(m), h.p[p]);
+            }
     return h;
+}
+
+// The lanes of the scan's last run publish the tile's map ...
+template <bool PACKED>
+__device__ __forceinline__ void post_map(const Tiling &tl, const Item &it, const Map4 &before, const Exchange &ex, int quad)
+{
+    if (it.step + 1 >= tl.ntiles || it.step % kGroup == kGroup - 1) return;     // nobody reads it
+    float4 *to = &tl.maps[(((long long)it.row * tl.ntiles + it.step) * tl.nblk + it.blk) * 32 + 2 * quad];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        F2 A = before.A[p], B = before.B[p];
+        const float4 v = ex.run[kRuns - 1][2 * quad + p];
+        compose_map<PACKED>(A, B, map_A(v), map_B(v));
+        post(to + p, pack_map(A, B));
+    }
+}
+// ... and, for a group's last tile, the state after it (h: entering the run).
+template <bool PACKED>
+__device__ __forceinline__ void post_state(const Tiling &tl, const Item &it, F4 h, const Exchange &ex, int quad, int *status)
+{
+    if (it.step + 1 >= tl.ntiles || it.step % kGroup != kGroup - 1) return;
+    if (*reinterpret_cast<volatile int *>(status) == kDevTimeout) return;
+    const int groups = (tl.ntiles + kGroup - 1) / kGroup;
+    float2 *to = &tl.states[(((long long)it.row * groups + it.step / kGroup) * tl.nblk + it.blk) * 32 + 2 * quad];
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {
+        const float4 v = ex.run[kRuns - 1][2 * quad + p];
+        float2 o;
+        split(apply_map<PACKED>(map_A(v), map_B(v), h.p[p]), o.x, o.y);
+        post(to + p, o);
+    }
 }
 
 // Copies tokens [t0, t0 + 2 kL) of one array, channels c0 .. c0 + 63, to
@@ -459,21 +499,15 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         }
         if (threadIdx.x == 0) sm.slot[(n + 2) & 3] = next;
         __syncthreads();
-        if (w != 0) fetch(sm.slot[(n + 2) & 3], stage);
-        if (w == 0) {
-            float2 start = make_float2(0.0f, 0.0f);
-            const int cp = it.blk * 64 + 2 * lane;
-            if (!PACKED && g.init && it.step < kGroup && cp < g.D)
-                start = make_float2(g.init[(long long)it.row * g.D + cp],
-                                    cp + 1 < g.D ? g.init[(long long)it.row * g.D + cp + 1] : 0.0f);
-            if (tl.ntiles > 1)
-                exchange<PACKED>(tl, it, lane, start, sm.ex, g.status);
-            else
-                sm.ex.state[lane] = start;
-        }
+        const Map4 before = runs_before<PACKED>(sm.ex, run, quad);
+        if (run == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
+        gather_maps<PACKED>(tl, it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
+        fetch(sm.slot[(n + 2) & 3], stage);
         __syncthreads();
-        if (w == 0) fetch(sm.slot[(n + 2) & 3], stage);
-        F4 h = enter_run<PACKED>(sm.ex, run, quad);
+        F4 h = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) h.p[p] = apply_map<PACKED>(before.A[p], before.B[p], h.p[p]);
+        if (run == kRuns - 1) post_state<PACKED>(tl, it, h, sm.ex, quad, g.status);
         if (!live || t0 >= g.T) continue;
 
         if (chunk_states && run == 0) {
