@@ -217,7 +217,7 @@ __device__ __forceinline__ int take_ticket(const Tiling &tl, int *slot)
 // ---------------------------------------------------------------- the scan kernels' tiles
 // A CTA of kWarps warps walks tiles of kTile tokens by 64 channels.  A lane has
 // four adjacent channels of a run of kL tokens, half a warp one run.
-constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kStages = 2, kThreads = 32 * kWarps;
+constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kThreads = 32 * kWarps;
 static_assert(kTile == SSD_GLR_CHUNK, "a tile starts at a chunk state");
 
 __device__ __forceinline__ float4 pack_map(F2 A, F2 B)
@@ -387,9 +387,9 @@ __device__ __forceinline__ RunMarks run_marks(const Marks<kTile> &m, int run, in
 }
 
 template <typename T> struct FwdSmem {
-    T in[kStages][kWarps][3][2 * kL][64];   // r, i, x
+    T in[kWarps][3][2 * kL][64];    // r, i, x
     Exchange ex;
-    int4 slot[4];                   // row, step, block of the next tiles; w: 0 when there are none
+    int4 slot[2];                   // row, step, block of this and the next tile; w: 0 when there is none
 };
 
 __device__ __forceinline__ int4 draw_item(const Tiling &tl, int total)
@@ -401,12 +401,12 @@ __device__ __forceinline__ int4 draw_item(const Tiling &tl, int total)
 
 // y (NULL: chunk states only), final_states and chunk_states may be NULL.
 //
-// CTAs stay on their SM and take tile after tile.  Each warp copies its own
-// runs, kStages tiles ahead, so HBM reads go on while the CTA computes and
-// waits for other tiles; the ticket of the tile after next is drawn while this
-// one is computed.
+// CTAs stay on their SM and take tile after tile.  The next tile's ticket is
+// drawn while this one's gates are computed, and each warp copies its runs of
+// the next tile as soon as its own are in registers, so HBM reads go on while
+// the CTA waits for other tiles and writes.
 template <typename T, int COPY, bool PACKED>
-__global__ void __launch_bounds__(kThreads, sizeof(T) == 2 ? 4 : 2)
+__global__ void __launch_bounds__(kThreads, 4)
 glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ final_states,
                float *__restrict__ chunk_states)
 {
@@ -417,11 +417,11 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int total = tl.rows * tl.ntiles * tl.nblk;
 
-    const auto fetch = [&](int4 it, int stage) {
+    const auto fetch = [&](int4 it) {
         if (it.w) {
             const int t0 = it.y * kTile + w * 2 * kL, c0 = it.z * 64;
             const long long row0 = (long long)it.x * g.T;
-            T(*in)[2 * kL][64] = sm.in[stage][w];
+            T(*in)[2 * kL][64] = sm.in[w];
             stage_runs<T, COPY>(in[0][0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
             stage_runs<T, COPY>(in[1][0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
             stage_runs<T, COPY>(in[2][0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
@@ -429,23 +429,21 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         copy_commit();
     };
 
-    if (threadIdx.x == 0)
-        for (int k = 0; k < kStages; ++k) sm.slot[k] = draw_item(tl, total);
+    if (threadIdx.x == 0) sm.slot[0] = draw_item(tl, total);
     __syncthreads();
-    for (int k = 0; k < kStages; ++k) fetch(sm.slot[k], k);
+    fetch(sm.slot[0]);
 
     for (int n = 0;; ++n) {
-        const int4 s4 = sm.slot[n & 3];
+        const int4 s4 = sm.slot[n & 1];
         if (!s4.w) break;
         const Item it{s4.x, s4.y, s4.z};
-        const int stage = n % kStages;
         int4 next = make_int4(0, 0, 0, 0);
         if (threadIdx.x == 0) next = draw_item(tl, total);
         const int c = it.blk * 64 + 4 * quad, t0 = it.step * kTile + run * kL, nc = g.D - c;
         const bool live = nc > 0;
         F4 rate = {f2(0.0f), f2(0.0f)};
         if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
-        copy_wait<kStages - 1>();
+        copy_wait<0>();
         __syncthreads();                            // every warp is done with the tile before
         RunMarks rm{0, 0};
         if constexpr (PACKED) {
@@ -461,7 +459,7 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
 
         F4 a[kL], b[kL];
-        T(*in)[2 * kL][64] = sm.in[stage][w];
+        T(*in)[2 * kL][64] = sm.in[w];
 #pragma unroll
         for (int j = 0; j < kL; ++j) {
             const int row = half * kL + j;
@@ -497,12 +495,12 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
             for (int j = 1; j < kL; ++j) compose_map<PACKED>(A, B, a[j].p[p], b[j].p[p]);
             sm.ex.run[run][2 * quad + p] = pack_map(A, B);
         }
-        if (threadIdx.x == 0) sm.slot[(n + 2) & 3] = next;
+        if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = next;
         __syncthreads();
         const Map4 before = runs_before<PACKED>(sm.ex, run, quad);
         if (run == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
         gather_maps<PACKED>(tl, it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
-        fetch(sm.slot[(n + 2) & 3], stage);
+        fetch(sm.slot[(n + 1) & 1]);
         __syncthreads();
         F4 h = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
 #pragma unroll
@@ -910,7 +908,7 @@ cudaError_t launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, 
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const long long items = (long long)tl.rows * tl.ntiles * tl.nblk;
-    const int grid = (int)std::min<long long>(items, (long long)sm_count() * (sizeof(T) == 2 ? 4 : 2));
+    const int grid = (int)std::min<long long>(items, (long long)sm_count() * 4);
     kernel<<<grid, kThreads, smem, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
     return cudaGetLastError();
 }
