@@ -22,8 +22,12 @@
 #include <initializer_list>
 #include <type_traits>
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "ssd_glr.cuh"
 #include "ssd_glr.h"
+#include "ssd_tc_prims.cuh"
 
 namespace ssd {
 namespace {
@@ -236,50 +240,71 @@ struct Exchange {
 };
 
 // A warp's share of the exchange between the tiles of a row, a channel pair a
-// lane: fetches kGroup / kWarps of the group's earlier tiles' maps (one round
-// trip to L2 when they are there) and leaves their composition in ex.tile; the
-// last warp also fetches the state after the group before.
+// lane: kGroup / kWarps of the group's earlier tiles' maps, whose composition
+// it leaves in ex.tile; the last warp also has the state after the group
+// before.  ask() sends for them, finish() waits until all are there: the round
+// trip to L2 passes while the tile's own maps are composed.
 template <bool PACKED>
-__device__ __forceinline__ void gather_maps(const Tiling &tl, const Item &it, int w, int lane, const float *row_start,
-                                            int D, Exchange &ex, int *status)
-{
-    constexpr int N = kGroup / kWarps;
-    const int in_group = it.step % kGroup, group = it.step / kGroup, npairs = tl.nblk * 32, pair = it.blk * 32 + lane;
-    const int cnt = min(max(in_group - w * N, 0), N);
-    const bool state = w == kWarps - 1 && group > 0;
-    if (w == kWarps - 1 && group == 0) {
-        const int c = 2 * pair;
-        ex.state[lane] = make_float2(row_start && c < D ? row_start[c] : 0.0f, row_start && c + 1 < D ? row_start[c + 1] : 0.0f);
-    }
-    if (cnt == 0 && !state) return;
-    const float4 *maps = &tl.maps[((long long)it.row * tl.ntiles + group * kGroup + w * N) * npairs + pair];
-    const float2 *before = &tl.states[((long long)it.row * ((tl.ntiles + kGroup - 1) / kGroup) + group - 1) * npairs + pair];
+struct Gather {
+    static constexpr int N = kGroup / kWarps;
+    const float4 *maps;
+    const float2 *before;
     uint4 m[N];
-    uint2 s = make_uint2(1, 1);
-    Patience wait;
-    bool all;
-    do {
-        all = true;
+    uint2 s;
+    int cnt;
+    bool state;
+
+    __device__ __forceinline__ void peek_all()
+    {
         if (state) s = peek(before);
 #pragma unroll
-        for (int k = 0; k < N; ++k) m[k] = k < cnt ? peek(maps + (long long)k * npairs) : make_uint4(1, 1, 1, 1);
-        all = written(s);
-#pragma unroll
-        for (int k = 0; k < N; ++k) all = all && written(m[k]);
-    } while (!all && wait.more(status));
-    if (cnt) {
-        float4 v = value_of(m[0]);
-        F2 A = map_A(v), B = map_B(v);
-#pragma unroll
-        for (int k = 1; k < N; ++k)
-            if (k < cnt) {
-                v = value_of(m[k]);
-                compose_map<PACKED>(A, B, map_A(v), map_B(v));
-            }
-        ex.tile[w][lane] = pack_map(A, B);
+        for (int k = 0; k < N; ++k)
+            if (k < cnt) m[k] = peek(maps + (size_t)k * stride);
     }
-    if (state) ex.state[lane] = value_of(s);
-}
+    int stride;
+
+    __device__ __forceinline__ void ask(const Tiling &tl, const Item &it, int w, int lane)
+    {
+        const int in_group = it.step % kGroup, group = it.step / kGroup, pair = it.blk * 32 + lane;
+        stride = tl.nblk * 32;
+        cnt = min(max(in_group - w * N, 0), N);
+        state = w == kWarps - 1 && group > 0;
+        maps = &tl.maps[((long long)it.row * tl.ntiles + group * kGroup + w * N) * stride + pair];
+        before = &tl.states[((long long)it.row * ((tl.ntiles + kGroup - 1) / kGroup) + group - 1) * stride + pair];
+        peek_all();
+    }
+
+    __device__ __forceinline__ void finish(const Item &it, int w, int lane, const float *row_start, int D, Exchange &ex,
+                                           int *status)
+    {
+        if (w == kWarps - 1 && !state) {
+            const int c = 2 * (it.blk * 32 + lane);
+            ex.state[lane] = make_float2(row_start && c < D ? row_start[c] : 0.0f,
+                                         row_start && c + 1 < D ? row_start[c + 1] : 0.0f);
+        }
+        if (cnt == 0 && !state) return;
+        Patience wait;
+        while (true) {
+            bool all = !state || written(s);
+#pragma unroll
+            for (int k = 0; k < N; ++k) all = all && (k >= cnt || written(m[k]));
+            if (all || !wait.more(status)) break;
+            peek_all();
+        }
+        if (cnt) {
+            float4 v = value_of(m[0]);
+            F2 A = map_A(v), B = map_B(v);
+#pragma unroll
+            for (int k = 1; k < N; ++k)
+                if (k < cnt) {
+                    v = value_of(m[k]);
+                    compose_map<PACKED>(A, B, map_A(v), map_B(v));
+                }
+            ex.tile[w][lane] = pack_map(A, B);
+        }
+        if (state) ex.state[lane] = value_of(s);
+    }
+};
 
 struct Map4 {
     F2 A[2], B[2];
@@ -350,8 +375,8 @@ __device__ __forceinline__ void post_state(const Tiling &tl, const Item &it, F4 
 }
 
 // Copies tokens [t0, t0 + 2 kL) of one array, channels c0 .. c0 + 63, to
-// dst[2 kL][64]; zeros outside the row or the channels.  COPY is what the rows'
-// alignment allows: 16 bytes, two elements, or one.  A warp's work.
+// dst[2 kL][64]; zeros outside the row or the channels.  For rows that TMA
+// cannot address: COPY is the bytes of two elements, or of one.  A warp's work.
 template <typename T, int COPY>
 __device__ __forceinline__ void stage_runs(T *dst, const T *row, long long stride, int t0, int T_, int c0, int D, int lane)
 {
@@ -386,15 +411,21 @@ __device__ __forceinline__ RunMarks run_marks(const Marks<kTile> &m, int run, in
     return {(f >> shift) & 0xffu, (l >> shift) & 0xffu};
 }
 
+// TMA descriptors of the inputs as (tokens, channels), boxes of kTile x 64.
+struct InputMaps {
+    CUtensorMap r, i, x, dy;
+};
+
 template <typename T> struct FwdSmem {
-    T in[kWarps][3][2 * kL][64];    // r, i, x
+    T in[3][kTile][64];             // r, i, x
+    uint64_t full;                  // the tile's copies have arrived
+    int abort;
     Exchange ex;
     int4 slot[2];                   // row, step, block of this and the next tile; w: 0 when there is none
 };
 
-__device__ __forceinline__ int4 draw_item(const Tiling &tl, int total)
+__device__ __forceinline__ int4 slot_of(const Tiling &tl, int ticket, int total)
 {
-    const int ticket = atomicAdd(tl.ticket, 1);
     const Item it = item_of(tl, ticket);
     return make_int4(it.row, it.step, it.blk, ticket < total);
 }
@@ -407,10 +438,10 @@ __device__ __forceinline__ int4 draw_item(const Tiling &tl, int total)
 // the CTA waits for other tiles and writes.
 template <typename T, int COPY, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 4)
-glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ final_states,
-               float *__restrict__ chunk_states)
+glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *__restrict__ y,
+               float *__restrict__ final_states, float *__restrict__ chunk_states)
 {
-    extern __shared__ __align__(16) char smem_raw[];
+    extern __shared__ __align__(128) char smem_raw[];
     FwdSmem<T> &sm = *reinterpret_cast<FwdSmem<T> *>(smem_raw);
     __shared__ Marks<PACKED ? kTile : 1> marks;
     constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
@@ -418,18 +449,35 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
     const int total = tl.rows * tl.ntiles * tl.nblk;
 
     const auto fetch = [&](int4 it) {
-        if (it.w) {
-            const int t0 = it.y * kTile + w * 2 * kL, c0 = it.z * 64;
-            const long long row0 = (long long)it.x * g.T;
-            T(*in)[2 * kL][64] = sm.in[w];
-            stage_runs<T, COPY>(in[0][0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
-            stage_runs<T, COPY>(in[1][0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
-            stage_runs<T, COPY>(in[2][0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
+        const int c0 = it.z * 64;
+        if constexpr (COPY == 16) {
+            if (threadIdx.x == 0 && it.w) {
+                const int t = it.x * g.T + it.y * kTile;
+                tc::mbar_arrive_expect_tx(&sm.full, sizeof(sm.in));
+                tc::tma_load_2d(sm.in[0], &maps.r, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[1], &maps.i, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[2], &maps.x, &sm.full, c0, t);
+            }
+        } else {
+            if (it.w) {
+                const int q0 = w * 2 * kL, t0 = it.y * kTile + q0;
+                const long long row0 = (long long)it.x * g.T;
+                stage_runs<T, COPY>(sm.in[0][q0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.in[1][q0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.in[2][q0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
+            }
+            copy_commit();
         }
-        copy_commit();
     };
 
-    if (threadIdx.x == 0) sm.slot[0] = draw_item(tl, total);
+    if (threadIdx.x == 0) {
+        sm.slot[0] = slot_of(tl, atomicAdd(tl.ticket, 1), total);
+        sm.abort = 0;
+        if constexpr (COPY == 16) {
+            tc::mbar_init(&sm.full, 1);
+            tc::mbar_fence_init();
+        }
+    }
     __syncthreads();
     fetch(sm.slot[0]);
 
@@ -437,13 +485,17 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         const int4 s4 = sm.slot[n & 1];
         if (!s4.w) break;
         const Item it{s4.x, s4.y, s4.z};
-        int4 next = make_int4(0, 0, 0, 0);
-        if (threadIdx.x == 0) next = draw_item(tl, total);
+        int next = 0;
+        if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
         const int c = it.blk * 64 + 4 * quad, t0 = it.step * kTile + run * kL, nc = g.D - c;
         const bool live = nc > 0;
         F4 rate = {f2(0.0f), f2(0.0f)};
         if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
-        copy_wait<0>();
+        if constexpr (COPY == 16) {
+            if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
+        } else {
+            copy_wait<0>();
+        }
         __syncthreads();                            // every warp is done with the tile before
         RunMarks rm{0, 0};
         if constexpr (PACKED) {
@@ -459,11 +511,10 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
         rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
 
         F4 a[kL], b[kL];
-        T(*in)[2 * kL][64] = sm.in[w];
 #pragma unroll
         for (int j = 0; j < kL; ++j) {
-            const int row = half * kL + j;
-            const F4 r4 = load4(&in[0][row][4 * quad]), i4 = load4(&in[1][row][4 * quad]), x4 = load4(&in[2][row][4 * quad]);
+            const int row = run * kL + j;
+            const F4 r4 = load_gates(&sm.in[0][row][4 * quad]), i4 = load_gates(&sm.in[1][row][4 * quad]), x4 = load4(&sm.in[2][row][4 * quad]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const Gate2 k = gate2(r4.p[p], i4.p[p], rate.p[p]);
@@ -488,6 +539,8 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
                     for (int p = 0; p < 2; ++p) b[j].p[p] = fma(a[j].p[p], h0.p[p], b[j].p[p]), a[j].p[p] = f2(0.0f);
                 }
         }
+        Gather<PACKED> others;
+        others.ask(tl, it, w, lane);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
             F2 A = a[0].p[p], B = b[0].p[p];
@@ -495,12 +548,12 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
             for (int j = 1; j < kL; ++j) compose_map<PACKED>(A, B, a[j].p[p], b[j].p[p]);
             sm.ex.run[run][2 * quad + p] = pack_map(A, B);
         }
-        if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = next;
+        if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
         __syncthreads();
         const Map4 before = runs_before<PACKED>(sm.ex, run, quad);
         if (run == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
-        gather_maps<PACKED>(tl, it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
         fetch(sm.slot[(n + 1) & 1]);
+        others.finish(it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
         __syncthreads();
         F4 h = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
 #pragma unroll
@@ -538,7 +591,6 @@ glr_fwd_kernel(GlrArgs g, Tiling tl, T *__restrict__ y, float *__restrict__ fina
             }
         }
     }
-    copy_wait<0>();
 }
 
 // One tile of L W = SSD_GLR_CHUNK tokens, the row's last tile first.  The
@@ -900,8 +952,35 @@ int copy_bytes(const ssd_glr_params &p, std::initializer_list<const void *> io, 
     return es;
 }
 
+// Tensor map of a (tokens, channels) array with rows `stride` elements apart.
+bool encode(CUtensorMap &m, const void *p, ssd_dtype t, long long tokens, int channels, long long stride)
+{
+    static const PFN_cuTensorMapEncodeTiled_v12000 fn = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void *f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            return nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    if (!fn) return false;
+    const cuuint64_t dim[2] = {(cuuint64_t)channels, (cuuint64_t)tokens};
+    const cuuint64_t pitch[1] = {(cuuint64_t)stride * elem_size(t)};
+    const cuuint32_t box[2] = {64, kTile}, one[2] = {1, 1};
+    return fn(&m, t == SSD_DTYPE_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2,
+              const_cast<void *>(p), dim, pitch, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_128B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool encode_inputs(InputMaps &m, const ssd_glr_params &p, const GlrArgs &g, const void *dy)
+{
+    const long long n = (long long)p.batch * p.seqlen;
+    return encode(m.r, g.r, p.io_dtype, n, g.D, g.rs) && encode(m.i, g.i, p.io_dtype, n, g.D, g.is) &&
+           encode(m.x, g.x, p.io_dtype, n, g.D, g.xs) && (!dy || encode(m.dy, dy, p.io_dtype, n, g.D, g.D));
+}
+
 template <typename T, int COPY, bool PACKED>
-cudaError_t launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+cudaError_t launch_fwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
 {
     const auto kernel = glr_fwd_kernel<T, COPY, PACKED>;
     const int smem = sizeof(FwdSmem<T>);
@@ -909,21 +988,21 @@ cudaError_t launch_fwd(const GlrArgs &g, const Tiling &tl, void *y, float *fin, 
     if (e != cudaSuccess) return e;
     const long long items = (long long)tl.rows * tl.ntiles * tl.nblk;
     const int grid = (int)std::min<long long>(items, (long long)sm_count() * 4);
-    kernel<<<grid, kThreads, smem, st>>>(g, tl, static_cast<T *>(y), fin, chunks);
+    kernel<<<grid, kThreads, smem, st>>>(maps, g, tl, static_cast<T *>(y), fin, chunks);
     return cudaGetLastError();
 }
 
 template <typename T>
-cudaError_t launch_fwd(const GlrArgs &g, int copy, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
+cudaError_t launch_fwd(const InputMaps &m, const GlrArgs &g, int copy, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
 {
     constexpr int P = 2 * sizeof(T), S = sizeof(T);
     if (g.cu)
-        return copy == 16  ? launch_fwd<T, 16, true>(g, tl, y, fin, chunks, st)
-               : copy == P ? launch_fwd<T, P, true>(g, tl, y, fin, chunks, st)
-                           : launch_fwd<T, S, true>(g, tl, y, fin, chunks, st);
-    return copy == 16  ? launch_fwd<T, 16, false>(g, tl, y, fin, chunks, st)
-           : copy == P ? launch_fwd<T, P, false>(g, tl, y, fin, chunks, st)
-                       : launch_fwd<T, S, false>(g, tl, y, fin, chunks, st);
+        return copy == 16  ? launch_fwd<T, 16, true>(m, g, tl, y, fin, chunks, st)
+               : copy == P ? launch_fwd<T, P, true>(m, g, tl, y, fin, chunks, st)
+                           : launch_fwd<T, S, true>(m, g, tl, y, fin, chunks, st);
+    return copy == 16  ? launch_fwd<T, 16, false>(m, g, tl, y, fin, chunks, st)
+           : copy == P ? launch_fwd<T, P, false>(m, g, tl, y, fin, chunks, st)
+                       : launch_fwd<T, S, false>(m, g, tl, y, fin, chunks, st);
 }
 
 cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_t st)
@@ -942,8 +1021,10 @@ cudaError_t run_fwd(const ssd_glr_params &p, const GlrArgs &g, void *y, float *f
     const cudaError_t e = cudaMemsetAsync(ws, 0, s.clear, st);
     if (e != cudaSuccess) return e;
     if (p.seqlen == 0) return fin ? run_copy(g, g.init, fin, st) : cudaSuccess;
-    return p.io_dtype == SSD_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(g, copy, s.tl, y, fin, chunks, st)
-                                        : launch_fwd<float>(g, copy, s.tl, y, fin, chunks, st);
+    InputMaps maps;
+    if (copy == 16 && !encode_inputs(maps, p, g, nullptr)) return cudaErrorUnknown;
+    return p.io_dtype == SSD_DTYPE_BF16 ? launch_fwd<__nv_bfloat16>(maps, g, copy, s.tl, y, fin, chunks, st)
+                                        : launch_fwd<float>(maps, g, copy, s.tl, y, fin, chunks, st);
 }
 
 struct BwdArgs {

@@ -130,13 +130,15 @@ __device__ __forceinline__ F2 each(F2 a, Op op)
 __device__ __forceinline__ F2 shown(float2 a) { return f2(a.x, a.y); }
 
 // Gates of two channels.  Four special-function operations an element: the two
-// sigmoids share one reciprocal (exponents clamped so that the product of the
+// sigmoids share one reciprocal (logits clamped so that the product of the
 // denominators stays below 2^125), and exp(-q) is taken on the FMA units, since
 // the special-function unit (16 lanes a clock and SM) would otherwise bound the
 // kernels.  1 - a^2 = (1 - a)(1 + a) needs 1 - a to full relative precision
 // for small q: q = n ln2 + f (two-term ln2, the usual argument reduction),
 // v = 1 - exp(-f) = f u with u a polynomial (degree 5, fitted on |f| <= 0.3467
 // at Chebyshev nodes, 2.4e-8 of u), s = 2^-n, a = s (1 - v), 1 - a = s v + (1 - s).
+//
+// The gates' logits are clamped below at -43 where they are loaded (load_gates).
 struct Gate2 {
     F2 a, m, inv_m, q;          // exp(-q), sqrt(1 - a^2), 1 / m (finite at m = 0), exp(A_log) sigmoid(r)
     F2 si, osi, osr;            // sigmoid(i), sigmoid(-i), sigmoid(-r)
@@ -145,7 +147,7 @@ struct Gate2 {
 __device__ __forceinline__ Gate2 gate2(F2 r, F2 i, F2 rate)
 {
     const F2 nlog2e = f2(-1.4426950408889634f), one = f2(1.0f), minus = f2(-1.0f);
-    const auto ex = [](float v) { return ex2_approx(min_nan(v, 62.0f)); };
+    const auto ex = [](float v) { return ex2_approx(v); };
     Gate2 g;
     const F2 er = each(mul(r, nlog2e), ex), ei = each(mul(i, nlog2e), ex);
     const F2 dr = add(er, one), di = add(ei, one);
@@ -189,6 +191,28 @@ __device__ __forceinline__ F4 load4(const float *p)         // 16-byte aligned
 __device__ __forceinline__ F4 load4(const __nv_bfloat16 *p) // 8-byte aligned
 {
     const uint2 u = *reinterpret_cast<const uint2 *>(p);
+    return {f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
+            f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))};
+}
+
+// Gate logits, at least -43 (NaN stays NaN): in bf16 two at a time.
+__device__ __forceinline__ F4 load_gates(const float *p)
+{
+    const auto clamp = [](float v) {
+        float o;
+        asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(v), "f"(-43.0f));
+        return o;
+    };
+    F4 v = load4(p);
+    v.p[0] = each(v.p[0], clamp), v.p[1] = each(v.p[1], clamp);
+    return v;
+}
+__device__ __forceinline__ F4 load_gates(const __nv_bfloat16 *p)
+{
+    uint2 u = *reinterpret_cast<const uint2 *>(p);
+    constexpr uint32_t low = 0xc22cc22cu;           // -43, -43
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(u.x) : "r"(low));
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(u.y) : "r"(low));
     return {f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
             f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))};
 }

@@ -61,7 +61,7 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity)
 // Polling loop of mbar_wait, kept out of line: the kernels have dozens of wait
 // sites, and one shared copy of the loop keeps their instruction footprint
 // (and so instruction-cache misses) small.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
+static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity, volatile int *abort, uint64_t limit_ns)
 {
     const uint64_t t0 = globaltimer_ns();
     for (uint32_t it = 1;; ++it) {
