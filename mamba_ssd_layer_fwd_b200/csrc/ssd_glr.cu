@@ -36,13 +36,10 @@ constexpr int kGroup = 16;          // tiles between two published states
 
 // Work split of one call (host and device).
 struct Tiling {
-    int ntiles, nblk, rows;         // tiles of a row, channel blocks, rows
-    int *ticket, *done;             // work counter; per channel block: finished CTAs (backward)
-    int *map_flag, *state_flag;     // [item], [row][group][blk]
+    int rows, ntiles, nblk;         // rows, tiles of a row, channel blocks
+    int *ticket;
     float4 *maps;                   // [row][tile][nblk * 32]: of channel pairs
     float2 *states;                 // [row][group][nblk * 32]
-    float2 *maps1;                  // [row][tile][D]
-    float *states1;
 };
 
 // The row's position of the CTA's tile, counted along the direction of the scan.
@@ -106,122 +103,11 @@ __device__ __forceinline__ void mark_sequences(const GlrArgs &g, Marks<TOKENS> &
     __syncthreads();
 }
 
-// Shared memory of one scan over a CTA's tile: C = 32 V channels, W warps.
-template <int V, int W>
-struct ScanSmem {
-    float2 run[W][32 * V];          // map of each warp's run
-    float2 tile[kGroup / 2][32 * V];  // maps of the group's earlier tiles, by pairs
-    float state[32 * V];            // state after the group before
-};
-
-// The exchange between the tiles of a row.  run[] holds the runs' maps in scan
-// order; publishes the tile's map (and, for a group's last tile, the state
-// after it) and returns in h the state entering run `w`.  `start` is the state
-// entering the row.
-template <int V, int W, bool PACKED>
-__device__ __forceinline__ void enter_state(const Tiling &tl, const Item &it, int D, int c, bool live, int w, int lane,
-                                            const float (&start)[V], ScanSmem<V, W> &sm, int *status, float (&h)[V])
-{
-    const int in_group = it.step % kGroup, group = it.step / kGroup;
-    const long long row_tile = (long long)it.row * tl.ntiles;
-    const int ngroups = (tl.ntiles + kGroup - 1) / kGroup;
-    if (tl.ntiles > 1) {
-        if (w == 0) {
-            if (it.step + 1 < tl.ntiles) {
-                float A[V], B[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-#pragma unroll
-                for (int k = 0; k < W; ++k)
-#pragma unroll
-                    for (int v = 0; v < V; ++v) {
-                        const float2 m = sm.run[k][lane * V + v];
-                        compose_map<PACKED>(A[v], B[v], m.x, m.y);
-                    }
-                if (live) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v)
-                        __stcg(&tl.maps1[(row_tile + it.step) * D + c + v], make_float2(A[v], B[v]));
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) st_release(&tl.map_flag[(row_tile + it.step) * tl.nblk + it.blk], 1);
-            }
-        }
-        // pairs of the group's earlier tiles, spread over the warps
-        for (int pair = w; pair * 2 < in_group; pair += W) {
-            float A[V], B[V];
-#pragma unroll
-            for (int v = 0; v < V; ++v) A[v] = 1.0f, B[v] = 0.0f;
-            const int t0 = group * kGroup + pair * 2, cnt = min(2, in_group - pair * 2);
-            bool ok = wait_flag(&tl.map_flag[(row_tile + t0) * tl.nblk + it.blk], status);
-            if (ok && cnt > 1) ok = wait_flag(&tl.map_flag[(row_tile + t0 + 1) * tl.nblk + it.blk], status);
-            if (ok && live) {
-                float2 m[2][V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    m[0][v] = __ldcg(&tl.maps1[(row_tile + t0) * D + c + v]);
-                    m[1][v] = cnt > 1 ? __ldcg(&tl.maps1[(row_tile + t0 + 1) * D + c + v]) : make_float2(1.0f, 0.0f);
-                }
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    A[v] = m[0][v].x, B[v] = m[0][v].y;
-                    compose_map<PACKED>(A[v], B[v], m[1][v].x, m[1][v].y);
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) sm.tile[pair][lane * V + v] = make_float2(A[v], B[v]);
-        }
-        if (w == W - 1 && group > 0) {
-            const long long at = (long long)it.row * ngroups + group - 1;
-            const bool ok = wait_flag(&tl.state_flag[at * tl.nblk + it.blk], status);
-#pragma unroll
-            for (int v = 0; v < V; ++v) sm.state[lane * V + v] = ok && live ? __ldcg(&tl.states1[at * D + c + v]) : 0.0f;
-        }
-        __syncthreads();
-    }
-#pragma unroll
-    for (int v = 0; v < V; ++v) h[v] = group > 0 ? sm.state[lane * V + v] : start[v];
-    for (int pair = 0; pair * 2 < in_group; ++pair)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float2 m = sm.tile[pair][lane * V + v];
-            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
-        }
-    for (int k = 0; k < w; ++k)
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float2 m = sm.run[k][lane * V + v];
-            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
-        }
-    if (w == W - 1 && in_group == kGroup - 1 && it.step + 1 < tl.ntiles &&
-        *reinterpret_cast<volatile int *>(status) != kDevTimeout) {
-        const long long at = (long long)it.row * ngroups + group;
-        if (live) {
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const float2 m = sm.run[W - 1][lane * V + v];
-                __stcg(&tl.states1[at * D + c + v], apply_map<PACKED>(m.x, m.y, h[v]));
-            }
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) st_release(&tl.state_flag[at * tl.nblk + it.blk], 1);
-    }
-}
-
-__device__ __forceinline__ int take_ticket(const Tiling &tl, int *slot)
-{
-    if (tl.ntiles == 1) return blockIdx.x;
-    if (threadIdx.x == 0) *slot = atomicAdd(tl.ticket, 1);
-    __syncthreads();
-    return *slot;
-}
-
 // ---------------------------------------------------------------- the scan kernels' tiles
 // A CTA of kWarps warps walks tiles of kTile tokens by 64 channels.  A lane has
 // four adjacent channels of a run of kL tokens, half a warp one run.
 constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kThreads = 32 * kWarps;
+static_assert(kWarps * 16 <= kRuns * 32, "room for the sums");
 static_assert(kTile == SSD_GLR_CHUNK, "a tile starts at a chunk state");
 
 __device__ __forceinline__ float4 pack_map(F2 A, F2 B)
@@ -312,7 +198,7 @@ struct Map4 {
 
 // Composition of the maps of the tile's runs before `run`, of a lane's channels.
 template <bool PACKED>
-__device__ __forceinline__ Map4 runs_before(const Exchange &ex, int run, int quad)
+__device__ __forceinline__ Map4 runs_before(const float4 (&maps)[kRuns][32], int run, int quad)
 {
     Map4 m = {{f2(1.0f), f2(1.0f)}, {f2(0.0f), f2(0.0f)}};
 #pragma unroll
@@ -320,7 +206,7 @@ __device__ __forceinline__ Map4 runs_before(const Exchange &ex, int run, int qua
         if (k < run)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const float4 v = ex.run[k][2 * quad + p];
+                const float4 v = maps[k][2 * quad + p];
                 compose_map<PACKED>(m.A[p], m.B[p], map_A(v), map_B(v));
             }
     return m;
@@ -517,9 +403,10 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
             const F4 r4 = load_gates(&sm.in[0][row][4 * quad]), i4 = load_gates(&sm.in[1][row][4 * quad]), x4 = load4(&sm.in[2][row][4 * quad]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const Gate2 k = gate2(r4.p[p], i4.p[p], rate.p[p]);
-                a[j].p[p] = k.a;
-                b[j].p[p] = mul(mul(k.m, k.si), x4.p[p]);
+                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
+                const Decay2 d = decay2(k.q);
+                a[j].p[p] = d.a;
+                b[j].p[p] = mul(mul(scale2(d.e, d.a).m, k.si), x4.p[p]);
             }
         }
         if (t0 + kL > g.T) {                        // behind the row's end: the state stays
@@ -550,7 +437,7 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         }
         if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
         __syncthreads();
-        const Map4 before = runs_before<PACKED>(sm.ex, run, quad);
+        const Map4 before = runs_before<PACKED>(sm.ex.run, run, quad);
         if (run == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
         fetch(sm.slot[(n + 1) & 1]);
         others.finish(it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
@@ -593,188 +480,286 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
     }
 }
 
-// One tile of L W = SSD_GLR_CHUNK tokens, the row's last tile first.  The
-// forward's states come from the chunk state and the runs' maps; the gradient
-// that enters a token from the later ones, c_t = a_t (dy_t + c_{t+1}), is a map
-// of the same kind scanned backwards.
-template <typename T, typename G, int V, int L, int W, bool PACKED>
-__global__ void __launch_bounds__(32 * W, 512 / (32 * W))
-glr_bwd_kernel(GlrArgs g, Tiling tl, const float *__restrict__ chunk_states, const T *__restrict__ dy,
-               const float *__restrict__ dfinal, G *__restrict__ dx, G *__restrict__ dr, G *__restrict__ di,
-               float *__restrict__ dA_part, float *__restrict__ dA, float *__restrict__ dinit)
+template <typename T> struct BwdSmem {
+    static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
+    T in[kStages][4][kTile][64];    // r, i, x, dy
+    uint64_t full;
+    int abort;
+    Exchange ex;                    // of the scan backwards: its runs are in reverse
+    float4 run[kRuns][32];          // maps of the forward scan's runs, later dA_log's sums by warp
+    float2 state[32];               // state that enters the tile
+    int4 slot[2];
+};
+
+// The row's last tile first.  The states come from the chunk state and the runs'
+// maps; the gradient that enters a token from the later ones, c_t = a_t (dy_t +
+// c_{t+1}), is a map of the same kind scanned backwards, so the exchange between
+// tiles is the forward's.  1 - a and the state before each token stay in
+// registers over it (so a is off by up to 2^-24 here, not by 2^-24 of itself:
+// gradients and recomputed states by that much of the value that is decayed);
+// the other gates are taken anew from the staged inputs (17 instructions an
+// element, against six more registers an element and half the warps).
+//
+// part: dA_log's sums of each tile, [row][tile][channels].
+template <typename T, typename G, int COPY, bool PACKED>
+__global__ void __launch_bounds__(kThreads, 3)
+glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, const float *__restrict__ chunk_states,
+               const T *__restrict__ dy, const float *__restrict__ dfinal, G *__restrict__ dx, G *__restrict__ dr,
+               G *__restrict__ di, float *__restrict__ part, float *__restrict__ dinit)
 {
-    static_assert(L * W == SSD_GLR_CHUNK, "a tile starts at a chunk state");
-    __shared__ ScanSmem<V, W> sm;
-    __shared__ float2 fwd_run[W][32 * V];
-    __shared__ Marks<PACKED ? L * W : 1> marks;
-    __shared__ int slot, is_last;
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const Item it = item_of(tl, take_ticket(tl, &slot));
-    const int tile = tl.ntiles - 1 - it.step;
-    const int c = (it.blk * 32 + lane) * V;
-    const bool live = c < g.D;
-    const int tile0 = tile * (L * W), t0 = tile0 + w * L;
-    const long long row0 = (long long)it.row * g.T;
+    extern __shared__ __align__(128) char smem_raw[];
+    BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(smem_raw);
+    __shared__ Marks<PACKED ? kTile : 1> marks;
+    constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
+    constexpr int kStages = BwdSmem<T>::kStages;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
+    const int back = kRuns - 1 - run;                       // the run in the order of the scan
+    const int total = tl.rows * tl.ntiles * tl.nblk;
 
-    Vec<T, V> xr[L], rr[L], ir[L], dr_[L];
-#pragma unroll
-    for (int j = 0; j < L; ++j)
-        if (live && t0 + j < g.T) {
-            const long long t = row0 + t0 + j;
-            rr[j] = load_stream<T, V>(static_cast<const T *>(g.r) + t * g.rs + c);
-            ir[j] = load_stream<T, V>(static_cast<const T *>(g.i) + t * g.is + c);
-            xr[j] = load_stream<T, V>(static_cast<const T *>(g.x) + t * g.xs + c);
-            dr_[j] = load_stream<T, V>(dy + t * g.D + c);
-        }
-    float rate[V], start[V], h[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        rate[v] = live ? expf(g.A_log[c + v]) : 0.0f;
-        start[v] = !PACKED && live && dfinal ? dfinal[(long long)it.row * g.D + c + v] : 0.0f;
-        h[v] = live && tile0 < g.T ? chunk_states[((long long)it.row * g.nchunk + tile) * g.D + c + v] : 0.0f;
-    }
-    if constexpr (PACKED)
-        mark_sequences(g, marks, tile0, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, true,
-                       [&](int s) {
-                           if (!dinit) return;
-                           for (int k = it.blk * 32 * V; k < min((it.blk + 1) * 32 * V, g.D); ++k)
-                               dinit[(long long)s * g.D + k] = dfinal ? dfinal[(long long)s * g.D + k] : 0.0f;
-                       });
-
-    Gate k[L][V];
-    float A[V], B[V], Ar[V], Br[V], dyv[L][V], x[L][V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) A[v] = Ar[v] = 1.0f, B[v] = Br[v] = 0.0f;
-#pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const bool in = live && t0 + j < g.T;
-        const int s = PACKED && in ? marks.first[w * L + j] : -1;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (in) {
-                k[j][v] = gate(to_f32(rr[j].v[v]), to_f32(ir[j].v[v]), rate[v]);
-                x[j][v] = to_f32(xr[j].v[v]);
-                dyv[j][v] = to_f32(dr_[j].v[v]);
-            } else {
-                k[j][v] = Gate{1.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                x[j][v] = dyv[j][v] = 0.0f;
+    const auto fetch = [&](int4 it, int stage) {
+        const int c0 = it.z * 64, tile0 = (tl.ntiles - 1 - it.y) * kTile;
+        if constexpr (COPY == 16) {
+            if (threadIdx.x == 0 && it.w) {
+                const int t = it.x * g.T + tile0;
+                tc::mbar_arrive_expect_tx(&sm.full, sizeof(sm.in[0]));
+                tc::tma_load_2d(sm.in[stage][0], &maps.r, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[stage][1], &maps.i, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[stage][2], &maps.x, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[stage][3], &maps.dy, &sm.full, c0, t);
             }
-            float fa = k[j][v].a, fb = k[j][v].m * k[j][v].si * x[j][v];
-            if (PACKED && s >= 0) {
-                fb = fmaf(fa, g.init ? g.init[(long long)s * g.D + c + v] : 0.0f, fb);
-                fa = 0.0f;
+        } else {
+            if (it.w) {
+                const int q0 = w * 2 * kL, t0 = tile0 + q0;
+                const long long row0 = (long long)it.x * g.T;
+                T(*in)[kTile][64] = sm.in[stage];
+                stage_runs<T, COPY>(in[0][q0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(in[1][q0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(in[2][q0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(in[3][q0], dy + row0 * g.D, g.D, t0, g.T, c0, g.D, lane);
             }
-            compose_map<PACKED>(A[v], B[v], fa, fb);
+            copy_commit();
+        }
+    };
+
+    if (threadIdx.x == 0) {
+        sm.slot[0] = slot_of(tl, atomicAdd(tl.ticket, 1), total);
+        sm.abort = 0;
+        if constexpr (COPY == 16) {
+            tc::mbar_init(&sm.full, 1);
+            tc::mbar_fence_init();
         }
     }
+    __syncthreads();
+    if (kStages == 2) fetch(sm.slot[0], 0);
+
+    for (int n = 0;; ++n) {
+        const int4 s4 = sm.slot[n & 1];
+        if (!s4.w) break;
+        const Item it{s4.x, s4.y, s4.z};
+        const int stage = n % kStages;
+        int next = 0;
+        if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
+        const int tile = tl.ntiles - 1 - it.step, c = it.blk * 64 + 4 * quad, t0 = tile * kTile + run * kL, nc = g.D - c;
+        const bool live = nc > 0;
+        F4 rate = {f2(0.0f), f2(0.0f)};
+        if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
+        float2 h0 = make_float2(0.0f, 0.0f);
+        if (w == 0) {
+            const int cp = it.blk * 64 + 2 * lane;
+            const float *from = chunk_states + ((long long)it.row * g.nchunk + tile) * g.D + cp;
+            if (cp < g.D) h0.x = from[0];
+            if (cp + 1 < g.D) h0.y = from[1];
+        }
+        if constexpr (kStages == 1) {
+            __syncthreads();                        // every warp is done with the tile before
+            fetch(s4, 0);
+        }
+        if constexpr (COPY == 16) {
+            if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
+        } else {
+            copy_wait<0>();
+        }
+        __syncthreads();
+        if (w == 0) sm.state[lane] = h0;
+        RunMarks rm{0, 0};
+        if constexpr (PACKED) {
+            mark_sequences(g, marks, tile * kTile, (long long)it.step * tl.nblk + it.blk,
+                           (long long)tl.ntiles * tl.nblk, true, [&](int s) {
+                               if (!dinit) return;
+                               for (int k = it.blk * 64; k < min((it.blk + 1) * 64, g.D); ++k)
+                                   dinit[(long long)s * g.D + k] = dfinal ? dfinal[(long long)s * g.D + k] : 0.0f;
+                           });
+            rm = run_marks(marks, run, lane);
+        }
+        const auto ex = [](float v) { return expf(v); };
+        rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
+        // a sequence's initial state, or the gradient of its final state, of the lane's channels
+        const auto of_sequence = [&](const float *p, int s) {
+            F4 v = {f2(0.0f), f2(0.0f)};
+            if (p && live) v = load4_global<ALIGN>(p + (long long)s * g.D + c, nc);
+            return v;
+        };
+        const T(*in)[kTile][64] = sm.in[stage];
+        const bool tail = t0 + kL > g.T;
+
+        F4 e[kL], b[kL];
 #pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-        const int s = PACKED && live && t0 + j < g.T ? marks.last[w * L + j] : -1;
+        for (int j = 0; j < kL; ++j) {
+            const int row = run * kL + j;
+            const F4 r4 = load_gates(&in[0][row][4 * quad]), i4 = load_gates(&in[1][row][4 * quad]), x4 = load4(&in[2][row][4 * quad]);
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (PACKED && s >= 0) {
-                dyv[j][v] += dfinal ? dfinal[(long long)s * g.D + c + v] : 0.0f;
-                Ar[v] = 0.0f;
-                Br[v] = k[j][v].a * dyv[j][v];
-            } else {
-                const float a = k[j][v].a;
-                compose_map<false>(Ar[v], Br[v], a, a * dyv[j][v]);
+            for (int p = 0; p < 2; ++p) {
+                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
+                e[j].p[p] = decay2(k.q).e;
+                b[j].p[p] = mul(mul(scale2(e[j].p[p], decay_of(e[j].p[p])).m, k.si), x4.p[p]);
             }
         }
-    }
+        if (tail) {                                 // behind the row's end: state and gradient stay
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-        fwd_run[w][lane * V + v] = make_float2(A[v], B[v]);
-        sm.run[W - 1 - w][lane * V + v] = make_float2(Ar[v], Br[v]);
-    }
-    __syncthreads();
-    float carry[V];
-    enter_state<V, W, PACKED>(tl, it, g.D, c, live, W - 1 - w, lane, start, sm, g.status, carry);
-    for (int q = 0; q < w; ++q)
+            for (int j = 0; j < kL; ++j)
+                if (t0 + j >= g.T)
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const float2 m = fwd_run[q][lane * V + v];
-            h[v] = apply_map<PACKED>(m.x, m.y, h[v]);
+                    for (int p = 0; p < 2; ++p) e[j].p[p] = b[j].p[p] = f2(0.0f);
         }
+        Gather<PACKED> others;
+        others.ask(tl, it, w, lane);
+        {
+            F2 A[2], B[2];
+#pragma unroll
+            for (int p = 0; p < 2; ++p) A[p] = f2(1.0f), B[p] = f2(0.0f);
+#pragma unroll
+            for (int j = 0; j < kL; ++j) {
+                F4 fa, fb = b[j];
+#pragma unroll
+                for (int p = 0; p < 2; ++p) fa.p[p] = decay_of(e[j].p[p]);
+                if (PACKED && (rm.first >> j & 1)) {
+                    const F4 v = of_sequence(g.init, marks.first[run * kL + j]);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) fb.p[p] = fma(fa.p[p], v.p[p], fb.p[p]), fa.p[p] = f2(0.0f);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) compose_map<PACKED>(A[p], B[p], fa.p[p], fb.p[p]);
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) sm.run[run][2 * quad + p] = pack_map(A[p], B[p]), A[p] = f2(1.0f), B[p] = f2(0.0f);
+#pragma unroll
+            for (int j = kL - 1; j >= 0; --j) {
+                F4 gy = load4(&in[3][run * kL + j][4 * quad]);
+                if (tail && t0 + j >= g.T) gy = {f2(0.0f), f2(0.0f)};
+                const bool last = PACKED && (rm.last >> j & 1);
+                if (last) {
+                    const F4 v = of_sequence(dfinal, marks.last[run * kL + j]);
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) gy.p[p] = add(gy.p[p], v.p[p]);
+                }
+#pragma unroll
+                for (int p = 0; p < 2; ++p) {
+                    const F2 a = decay_of(e[j].p[p]);
+                    compose_map<PACKED>(A[p], B[p], last ? f2(0.0f) : a, mul(a, gy.p[p]));
+                }
+            }
+#pragma unroll
+            for (int p = 0; p < 2; ++p) sm.ex.run[back][2 * quad + p] = pack_map(A[p], B[p]);
+        }
+        if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
+        __syncthreads();
+        const Map4 before = runs_before<PACKED>(sm.ex.run, back, quad);
+        if (back == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
+        if (kStages == 2) fetch(sm.slot[(n + 1) & 1], (n + 1) & 1);
+        F4 h;
+        {
+            const Map4 m = runs_before<PACKED>(sm.run, run, quad);
+            const float4 v = *reinterpret_cast<const float4 *>(&sm.state[2 * quad]);
+            h.p[0] = apply_map<PACKED>(m.A[0], m.B[0], f2(v.x, v.y));
+            h.p[1] = apply_map<PACKED>(m.A[1], m.B[1], f2(v.z, v.w));
+        }
+#pragma unroll
+        for (int j = 0; j < kL; ++j) {              // b[j] <- the state before token j
+            if (PACKED && (rm.first >> j & 1)) h = of_sequence(g.init, marks.first[run * kL + j]);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                const F2 after = fma(decay_of(e[j].p[p]), h.p[p], b[j].p[p]);
+                b[j].p[p] = h.p[p];
+                h.p[p] = after;
+            }
+        }
+        others.finish(it, w, lane, !PACKED && dfinal ? dfinal + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
+        __syncthreads();
+        F4 carry = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
+#pragma unroll
+        for (int p = 0; p < 2; ++p) carry.p[p] = apply_map<PACKED>(before.A[p], before.B[p], carry.p[p]);
+        if (back == kRuns - 1) post_state<PACKED>(tl, it, carry, sm.ex, quad, g.status);
 
-    float before[L][V], dAs[V];
+        F4 sum = {f2(0.0f), f2(0.0f)};
+        long long at = ((long long)it.row * g.T + t0 + kL - 1) * g.D + c;
 #pragma unroll
-    for (int j = 0; j < L; ++j) {
-        const int s = PACKED && live && t0 + j < g.T ? marks.first[w * L + j] : -1;
+        for (int j = kL - 1; j >= 0; --j, at -= g.D) {
+            if (tail && t0 + j >= g.T) continue;
+            const int row = run * kL + j;
+            const F4 r4 = load_gates(&in[0][row][4 * quad]), i4 = load_gates(&in[1][row][4 * quad]);
+            const F4 x4 = load4(&in[2][row][4 * quad]);
+            F4 gy = load4(&in[3][row][4 * quad]);
+            if (PACKED && (rm.last >> j & 1)) carry = of_sequence(dfinal, marks.last[row]);
+            F4 ox, oi, orr;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (PACKED && s >= 0) h[v] = g.init ? g.init[(long long)s * g.D + c + v] : 0.0f;
-            before[j][v] = h[v];
-            h[v] = fmaf(k[j][v].a, h[v], k[j][v].m * k[j][v].si * x[j][v]);
+            for (int p = 0; p < 2; ++p) {
+                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
+                const F2 a = decay_of(e[j].p[p]);
+                const Scale2 sc = scale2(e[j].p[p], a);
+                const F2 gt = add(gy.p[p], carry.p[p]), gs = mul(gt, k.si), ga = mul(gt, a);
+                ox.p[p] = mul(gs, sc.m);
+                oi.p[p] = mul(mul(ox.p[p], x4.p[p]), k.osi);
+                // q (a^2 / m) gs x - q a g h, with q / m finite as q -> 0
+                const F2 t = mul(mul(a, sc.inv_m), mul(gs, x4.p[p]));
+                const F2 dqq = mul(k.q, fma(a, t, mul(ga, mul(b[j].p[p], f2(-1.0f)))));
+                orr.p[p] = mul(dqq, k.osr);
+                sum.p[p] = add(sum.p[p], dqq);
+                carry.p[p] = ga;
+            }
+            if (live) {
+                store4<ALIGN>(dx + at, ox, nc);
+                store4<ALIGN>(di + at, oi, nc);
+                store4<ALIGN>(dr + at, orr, nc);
+                if (dinit) {
+                    const int s = PACKED ? (rm.first >> j & 1 ? marks.first[row] : -1) : (t0 + j == 0 ? it.row : -1);
+                    if (s >= 0) store4<ALIGN>(dinit + (long long)s * g.D + c, carry, nc);
+                }
+            }
+        }
+        float4 v;
+        split(sum.p[0], v.x, v.y), split(sum.p[1], v.z, v.w);
+        v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+        v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+        if (half == 0) sm.run[0][w * 16 + quad] = v;
+        __syncthreads();
+        if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) {
+            const float *col = &sm.run[0][0].x + threadIdx.x;
+            part[((long long)it.row * tl.ntiles + tile) * g.D + it.blk * 64 + threadIdx.x] =
+                (col[0] + col[64]) + (col[128] + col[192]);
         }
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v) dAs[v] = 0.0f;
-#pragma unroll
-    for (int j = L - 1; j >= 0; --j) {
-        if (!live || t0 + j >= g.T) continue;
-        const bool cut = PACKED && marks.last[w * L + j] >= 0;
-        float o1[V], o2[V], o3[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const Gate &q = k[j][v];
-            const float gt = cut ? dyv[j][v] : dyv[j][v] + carry[v];
-            const float gs = gt * q.si;
-            o1[v] = gs * q.m;
-            o2[v] = o1[v] * x[j][v] * q.osi;
-            // q dm/dq = q a^2 / m, finite as q -> 0
-            const float dqq = q.q * q.a * (q.a * q.inv_m * gs * x[j][v] - gt * before[j][v]);
-            o3[v] = dqq * q.osr;
-            dAs[v] += dqq;
-            carry[v] = q.a * gt;
-        }
-        const long long at = (row0 + t0 + j) * g.D + c;
-        store_vec<G, V>(dx + at, o1);
-        store_vec<G, V>(di + at, o2);
-        store_vec<G, V>(dr + at, o3);
-        if (dinit) {
-            const int s = PACKED ? marks.first[w * L + j] : (t0 + j == 0 ? it.row : -1);
-            if (s >= 0) store_vec<float, V>(dinit + (long long)s * g.D + c, carry);
-        }
-    }
+}
 
-    // dA_log: over the runs here, over tiles and rows by the channel block's last CTA
-    float *red = &fwd_run[0][0].x;
-    __syncthreads();
+// dA_log: the sum of the tiles' parts.  A CTA has 32 channels; eight warps take
+// every eighth tile and their sums are added in order.
+__global__ void __launch_bounds__(256) glr_dA_kernel(int n, int D, const float *__restrict__ part, float *__restrict__ dA)
+{
+    __shared__ float sums[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+    float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (c < D) {
+        int k = w;
+        for (; k + 24 < n; k += 32)
 #pragma unroll
-    for (int v = 0; v < V; ++v) red[w * 32 * V + lane * V + v] = dAs[v];
-    __syncthreads();
-    const int total = tl.rows * tl.ntiles, cl = threadIdx.x;
-    float part = 0.0f;
-    if (cl < 32 * V && it.blk * 32 * V + cl < g.D) {
-        for (int q = 0; q < W; ++q) part += red[q * 32 * V + cl];
-        if (total == 1)
-            dA[it.blk * 32 * V + cl] = part;
-        else
-            __stcg(&dA_part[((long long)it.row * tl.ntiles + tile) * g.D + it.blk * 32 * V + cl], part);
+            for (int u = 0; u < 4; ++u) s[u] += part[(long long)(k + 8 * u) * D + c];
+        for (; k < n; k += 8) s[0] += part[(long long)k * D + c];
     }
-    if (total == 1) return;
-    __threadfence();
+    sums[w][lane] = (s[0] + s[1]) + (s[2] + s[3]);
     __syncthreads();
-    if (threadIdx.x == 0) is_last = atomicAdd(&tl.done[it.blk], 1) == total - 1;
-    __syncthreads();
-    if (!is_last) return;
-    __threadfence();
-    float sum[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) sum[v] = 0.0f;
-    if (live)
-        for (int q = w; q < total; q += W)
-#pragma unroll
-            for (int v = 0; v < V; ++v) sum[v] += __ldcg(&dA_part[(long long)q * g.D + c + v]);
-    __syncthreads();
-#pragma unroll
-    for (int v = 0; v < V; ++v) red[w * 32 * V + lane * V + v] = sum[v];
-    __syncthreads();
-    if (cl < 32 * V && it.blk * 32 * V + cl < g.D) {
-        part = 0.0f;
-        for (int q = 0; q < W; ++q) part += red[q * 32 * V + cl];
-        dA[it.blk * 32 * V + cl] = part;
+    if (w == 0 && c < D) {
+        float v = 0.0f;
+        for (int k = 0; k < 8; ++k) v += sums[k][lane];
+        dA[c] = v;
     }
 }
 
@@ -853,76 +838,46 @@ GlrArgs args_of(const ssd_glr_params &p, const void *x, const void *r, const voi
     return g;
 }
 
-// Tile shapes: tokens a tile; channels a block is 32 V, V = 1 or 2.
-constexpr int kBwdL = 4, kBwdW = 16;
-
-// Workspace of one scan: status word, counters and flags (cleared together),
-// then maps and states.  Sized for V = 1, the most channel blocks.
+// Workspace of one scan: status word, ticket counter, and the maps and states
+// that tiles hand on (all cleared before a call).
 struct Scan {
     Tiling tl;
-    size_t clear, bytes;
+    size_t bytes;
 };
 
-Scan scan_of(const ssd_glr_params &p, int tile_tokens, int V, bool bwd, char *ws)
+Scan scan_of(const ssd_glr_params &p, char *ws)
 {
     Scan s{};
     Tiling &t = s.tl;
     t.rows = p.batch;
-    t.ntiles = (int)(((int64_t)p.seqlen + tile_tokens - 1) / tile_tokens);
-    t.nblk = (p.channels + 32 * V - 1) / (32 * V);
-    const size_t groups = (size_t)t.rows * ((t.ntiles + kGroup - 1) / kGroup);
-    const size_t items = (size_t)t.rows * t.ntiles * t.nblk;
-    size_t off = sizeof(int);
-    const auto take = [&](size_t n) { const size_t at = off; off += n * sizeof(int); return reinterpret_cast<int *>(ws + at); };
-    t.ticket = take(1);
-    if (bwd) t.done = take(t.nblk);
-    if (t.ntiles > 1) {
-        t.map_flag = take(items);
-        t.state_flag = take(groups * t.nblk);
-    }
-    off = align_up(off);
+    t.ntiles = (int)chunks_of(p);
+    t.nblk = (p.channels + 63) / 64;
+    t.ticket = reinterpret_cast<int *>(ws + sizeof(int));
+    size_t off = kAlign;
     if (t.ntiles > 1) {
         t.maps = reinterpret_cast<float4 *>(ws + off);
-        t.maps1 = reinterpret_cast<float2 *>(ws + off);
-        off = align_up(off + items * 32 * sizeof(float4));
+        off = align_up(off + (size_t)t.rows * t.ntiles * t.nblk * 32 * sizeof(float4));
         t.states = reinterpret_cast<float2 *>(ws + off);
-        t.states1 = reinterpret_cast<float *>(ws + off);
-        off = align_up(off + groups * t.nblk * 32 * sizeof(float2));
+        off = align_up(off + (size_t)t.rows * ((t.ntiles + kGroup - 1) / kGroup) * t.nblk * 32 * sizeof(float2));
     }
-    s.clear = off;
     s.bytes = off;
     return s;
 }
 
+// Backward: the scan's part (used by the recomputed forward first), dA_log's
+// parts, and the chunk states where the caller has none.
 struct BwdLayout {
-    size_t scan, part, chunks, total;
+    size_t part, chunks, total;
 };
 
 BwdLayout bwd_layout(const ssd_glr_params &p, bool with_chunks)
 {
-    BwdLayout l{};
-    const size_t n = (size_t)p.batch * chunks_of(p) * p.channels * sizeof(float);
-    l.part = scan_of(p, kBwdL * kBwdW, 1, true, nullptr).bytes;
-    l.chunks = align_up(l.part + n);
-    l.total = with_chunks ? l.chunks : align_up(l.chunks + n);
-    const size_t f = scan_of(p, kTile, 2, false, nullptr).bytes;
-    if (!with_chunks && f > l.chunks) {          // the forward's scan runs first, in the same place
-        l.chunks = f;
-        l.total = align_up(f + n);
-    }
+    const size_t n = align_up((size_t)p.batch * chunks_of(p) * p.channels * sizeof(float));
+    BwdLayout l;
+    l.part = scan_of(p, nullptr).bytes;
+    l.chunks = l.part + n;
+    l.total = with_chunks ? l.chunks : l.chunks + n;
     return l;
-}
-
-// Channels a lane: as many as the rows' alignment allows.
-int width_of(const ssd_glr_params &p, std::initializer_list<const void *> io, std::initializer_list<const void *> f32)
-{
-    const size_t es = elem_size(p.io_dtype);
-    if (p.channels % 2 || p.x_stride % 2 || p.r_stride % 2 || p.i_stride % 2) return 1;
-    for (const void *q : io)
-        if (!aligned(q, 2 * es)) return 1;
-    for (const void *q : f32)
-        if (!aligned(q, 8)) return 1;
-    return 2;
 }
 
 int sm_count()
@@ -1017,8 +972,8 @@ cudaError_t run_fwd(const ssd_glr_params &p, const GlrArgs &g, void *y, float *f
                     cudaStream_t st)
 {
     const int copy = copy_bytes(p, {g.x, g.r, g.i, y}, {g.A_log, g.init, fin, chunks});
-    const Scan s = scan_of(p, kTile, 2, false, ws);
-    const cudaError_t e = cudaMemsetAsync(ws, 0, s.clear, st);
+    const Scan s = scan_of(p, ws);
+    const cudaError_t e = cudaMemsetAsync(ws, 0, s.bytes, st);
     if (e != cudaSuccess) return e;
     if (p.seqlen == 0) return fin ? run_copy(g, g.init, fin, st) : cudaSuccess;
     InputMaps maps;
@@ -1035,18 +990,33 @@ struct BwdArgs {
     float *part, *dA, *dinit;
 };
 
-template <typename T, typename G, int V>
-void launch_bwd(const GlrArgs &g, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
+template <typename T, typename G, int COPY, bool PACKED>
+cudaError_t launch_bwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
 {
-    const unsigned grid = (unsigned)((size_t)tl.rows * tl.ntiles * tl.nblk);
-    const T *dy = static_cast<const T *>(b.dy);
-    G *dx = static_cast<G *>(b.dx), *dr = static_cast<G *>(b.dr), *di = static_cast<G *>(b.di);
+    const auto kernel = glr_bwd_kernel<T, G, COPY, PACKED>;
+    const int smem = sizeof(BwdSmem<T>);
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const long long items = (long long)tl.rows * tl.ntiles * tl.nblk;
+    const int grid = (int)std::min<long long>(items, (long long)sm_count() * 3);
+    kernel<<<grid, kThreads, smem, st>>>(maps, g, tl, b.chunks, static_cast<const T *>(b.dy), b.dfinal,
+                                         static_cast<G *>(b.dx), static_cast<G *>(b.dr), static_cast<G *>(b.di), b.part,
+                                         b.dinit);
+    glr_dA_kernel<<<(g.D + 31) / 32, 256, 0, st>>>(tl.rows * tl.ntiles, g.D, b.part, b.dA);
+    return cudaGetLastError();
+}
+
+template <typename T, typename G>
+cudaError_t launch_bwd(const InputMaps &m, const GlrArgs &g, int copy, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
+{
+    constexpr int P = 2 * sizeof(T), S = sizeof(T);
     if (g.cu)
-        glr_bwd_kernel<T, G, V, kBwdL, kBwdW, true><<<grid, 32 * kBwdW, 0, st>>>(g, tl, b.chunks, dy, b.dfinal, dx, dr,
-                                                                                 di, b.part, b.dA, b.dinit);
-    else
-        glr_bwd_kernel<T, G, V, kBwdL, kBwdW, false><<<grid, 32 * kBwdW, 0, st>>>(g, tl, b.chunks, dy, b.dfinal, dx, dr,
-                                                                                  di, b.part, b.dA, b.dinit);
+        return copy == 16  ? launch_bwd<T, G, 16, true>(m, g, tl, b, st)
+               : copy == P ? launch_bwd<T, G, P, true>(m, g, tl, b, st)
+                           : launch_bwd<T, G, S, true>(m, g, tl, b, st);
+    return copy == 16  ? launch_bwd<T, G, 16, false>(m, g, tl, b, st)
+           : copy == P ? launch_bwd<T, G, P, false>(m, g, tl, b, st)
+                       : launch_bwd<T, G, S, false>(m, g, tl, b, st);
 }
 
 }  // namespace
@@ -1058,7 +1028,7 @@ extern "C" {
 
 size_t ssd_glr_fwd_workspace_size(const ssd_glr_params *p)
 {
-    return validate(p) == SSD_OK ? scan_of(*p, kTile, 2, false, nullptr).bytes : 0;
+    return validate(p) == SSD_OK ? scan_of(*p, nullptr).bytes : 0;
 }
 
 size_t ssd_glr_bwd_workspace_size(const ssd_glr_params *p, int with_chunk_states)
@@ -1118,25 +1088,24 @@ ssd_status ssd_glr_bwd(const ssd_glr_params *p, const void *x, const void *r, co
         if (run_fwd(*p, g, nullptr, nullptr, c, ws, st) != cudaSuccess) return SSD_ERR_CUDA;
         b.chunks = c;
     }
-    const size_t ga = 2 * gs;
-    int V = width_of(*p, {x, r, i, dy}, {dinitial_states});
-    if (!aligned(dx, ga) || !aligned(dr, ga) || !aligned(di, ga)) V = 1;
-    const Scan s = scan_of(*p, kBwdL * kBwdW, V, true, ws);
-    if (cudaMemsetAsync(ws, 0, s.clear, st) != cudaSuccess) return SSD_ERR_CUDA;
+    const Scan s = scan_of(*p, ws);
+    if (cudaMemsetAsync(ws, 0, s.bytes, st) != cudaSuccess) return SSD_ERR_CUDA;
     if (p->seqlen == 0) {
         if (cudaMemsetAsync(dA_log, 0, p->channels * sizeof(float), st) != cudaSuccess) return SSD_ERR_CUDA;
         const cudaError_t e = dinitial_states ? run_copy(g, dfinal_states, dinitial_states, st) : cudaSuccess;
         return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
     }
+    int copy = copy_bytes(*p, {x, r, i, dy}, {A_log, initial_states, dfinal_states, dinitial_states});
+    for (const void *q : {dx, dr, di})              // stored four (two) channels at a time
+        while (copy > (int)es && !aligned(q, copy == 16 ? 4 * gs : 2 * gs)) copy = copy == 16 ? (int)(2 * es) : (int)es;
+    InputMaps maps;
+    if (copy == 16 && !encode_inputs(maps, *p, g, dy)) return SSD_ERR_CUDA;
     typedef __nv_bfloat16 H;
-    const bool bf = p->io_dtype == SSD_DTYPE_BF16, gb = p->grad_dtype == SSD_DTYPE_BF16;
-    if (bf && gb && V == 2) launch_bwd<H, H, 2>(g, s.tl, b, st);
-    else if (bf && gb) launch_bwd<H, H, 1>(g, s.tl, b, st);
-    else if (bf && V == 2) launch_bwd<H, float, 2>(g, s.tl, b, st);
-    else if (bf) launch_bwd<H, float, 1>(g, s.tl, b, st);
-    else if (V == 2) launch_bwd<float, float, 2>(g, s.tl, b, st);
-    else launch_bwd<float, float, 1>(g, s.tl, b, st);
-    return cudaGetLastError() == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
+    const bool bf = p->io_dtype == SSD_DTYPE_BF16;
+    const cudaError_t e = bf && p->grad_dtype == SSD_DTYPE_BF16 ? launch_bwd<H, H>(maps, g, copy, s.tl, b, st)
+                          : bf                                  ? launch_bwd<H, float>(maps, g, copy, s.tl, b, st)
+                                                                : launch_bwd<float, float>(maps, g, copy, s.tl, b, st);
+    return e == cudaSuccess ? SSD_OK : SSD_ERR_CUDA;
 }
 
 ssd_status ssd_glr_step(const ssd_glr_step_params *p, const void *x, const void *r, const void *i, const float *A_log,

@@ -130,25 +130,19 @@ __device__ __forceinline__ F2 each(F2 a, Op op)
 __device__ __forceinline__ F2 shown(float2 a) { return f2(a.x, a.y); }
 
 // Gates of two channels.  Four special-function operations an element: the two
-// sigmoids share one reciprocal (logits clamped so that the product of the
-// denominators stays below 2^125), and exp(-q) is taken on the FMA units, since
-// the special-function unit (16 lanes a clock and SM) would otherwise bound the
-// kernels.  1 - a^2 = (1 - a)(1 + a) needs 1 - a to full relative precision
-// for small q: q = n ln2 + f (two-term ln2, the usual argument reduction),
-// v = 1 - exp(-f) = f u with u a polynomial (degree 5, fitted on |f| <= 0.3467
-// at Chebyshev nodes, 2.4e-8 of u), s = 2^-n, a = s (1 - v), 1 - a = s v + (1 - s).
-//
-// The gates' logits are clamped below at -43 where they are loaded (load_gates).
-struct Gate2 {
-    F2 a, m, inv_m, q;          // exp(-q), sqrt(1 - a^2), 1 / m (finite at m = 0), exp(A_log) sigmoid(r)
+// sigmoids share one reciprocal (logits clamped at -43 where they are loaded,
+// so that the product of the denominators stays below 2^125), and exp(-q) is
+// taken on the FMA units, since the special-function unit (16 lanes a clock and
+// SM) would otherwise bound the kernels.
+struct Sigmoids2 {
+    F2 q;                       // exp(A_log) sigmoid(r)
     F2 si, osi, osr;            // sigmoid(i), sigmoid(-i), sigmoid(-r)
 };
-
-__device__ __forceinline__ Gate2 gate2(F2 r, F2 i, F2 rate)
+__device__ __forceinline__ Sigmoids2 sigmoids2(F2 r, F2 i, F2 rate)
 {
-    const F2 nlog2e = f2(-1.4426950408889634f), one = f2(1.0f), minus = f2(-1.0f);
+    const F2 nlog2e = f2(-1.4426950408889634f), one = f2(1.0f);
     const auto ex = [](float v) { return ex2_approx(v); };
-    Gate2 g;
+    Sigmoids2 g;
     const F2 er = each(mul(r, nlog2e), ex), ei = each(mul(i, nlog2e), ex);
     const F2 dr = add(er, one), di = add(ei, one);
     const F2 inv = each(mul(dr, di), [](float v) { return rcp_approx(v); });
@@ -157,23 +151,46 @@ __device__ __forceinline__ Gate2 gate2(F2 r, F2 i, F2 rate)
     g.osr = mul(er, sr);
     g.osi = mul(ei, g.si);
     g.q = each(mul(rate, sr), [](float v) { return min_nan(v, 87.0f); });
-    const F2 k = fma(g.q, f2(1.4426950408889634f), f2(12582912.0f));     // 1.5 * 2^23: low bits are rint(q log2 e)
+    return g;
+}
+
+// 1 - exp(-q), to full relative precision also for small q (1 - a^2 needs it):
+// q = n ln2 + f (two-term ln2, the usual argument reduction), v = 1 - exp(-f) =
+// f u with u a polynomial (degree 5, fitted on |f| <= 0.3467 at Chebyshev
+// nodes, 2.4e-8 of u), s = 2^-n, e = 1 - exp(-q) = s v + (1 - s) and
+// a = exp(-q) = s (1 - v), each to a few roundings of its own size.
+struct Decay2 {
+    F2 a, e;
+};
+__device__ __forceinline__ Decay2 decay2(F2 q)
+{
+    const F2 k = fma(q, f2(1.4426950408889634f), f2(12582912.0f));       // 1.5 * 2^23: low bits are rint(q log2 e)
     const F2 n = add(k, f2(-12582912.0f));
-    F2 f = fma(n, f2(-0.693359375f), g.q);                               // ln2 = 0.693359375 - 2.12194440e-4
+    F2 f = fma(n, f2(-0.693359375f), q);                                 // ln2 = 0.693359375 - 2.12194440e-4
     f = fma(n, f2(2.12194440e-4f), f);
     const F2 s = each(k, [](float v) { return __int_as_float(__float_as_int(v) * -(1 << 23) + (127 << 23)); });
     F2 u = fma(f, f2(-1.39337e-3f), f2(8.36319e-3f));
     u = fma(u, f, f2(-4.166646e-2f));
     u = fma(u, f, f2(0.16666577f));
     u = fma(u, f, f2(-0.5f));
-    u = fma(u, f, one);
-    const F2 v = mul(u, f);
-    g.a = mul(s, fma(v, minus, one));
-    const F2 e = fma(s, v, fma(s, minus, one));
-    const F2 w = fma(e, add(g.a, one), f2(1.17549435e-38f));             // 1 - a^2, kept off 0
-    g.inv_m = each(w, [](float x) { return rsqrt_approx(x); });
-    g.m = mul(w, g.inv_m);
-    return g;
+    u = fma(u, f, f2(1.0f));
+    const F2 v = mul(u, f), minus = f2(-1.0f), one = f2(1.0f);
+    return {mul(s, fma(v, minus, one)), fma(s, v, fma(s, minus, one))};
+}
+// a from e alone, to half a step of 1
+__device__ __forceinline__ F2 decay_of(F2 e) { return fma(e, f2(-1.0f), f2(1.0f)); }
+
+// m = sqrt(1 - a^2) = sqrt(e (1 + a)) and 1 / m (finite at m = 0: the radicand is kept off 0)
+struct Scale2 {
+    F2 m, inv_m;
+};
+__device__ __forceinline__ Scale2 scale2(F2 e, F2 a)
+{
+    const F2 w = fma(e, add(a, f2(1.0f)), f2(1.17549435e-38f));
+    Scale2 o;
+    o.inv_m = each(w, [](float x) { return rsqrt_approx(x); });
+    o.m = mul(w, o.inv_m);
+    return o;
 }
 
 // Four adjacent channels, as two pairs.  ALIGN is the elements that the

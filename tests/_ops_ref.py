@@ -7,6 +7,9 @@ of float32, relative).  Outputs in bf16 may be off by half a step of bf16 more:
 import torch
 
 U = 2.0 ** -24
+# The kernels take m = sqrt(w + 2^-126) for sqrt(w), w = 1 - a^2, so that 1 / m is finite: off by at most
+# sqrt(2^-126) = 2^-63, which is what is left of it at w = 0.
+M0 = 2.0 ** -63
 
 
 def half_step(dtype) -> float:
@@ -64,17 +67,30 @@ class Glr:
         self.eh, self.ebefore = torch.zeros_like(x), torch.zeros_like(x)
         self.final, self.efinal = init.clone(), torch.zeros_like(init)
         bt = self.m * self.si * x
+        m0 = 2 * M0 * (self.si * x).abs()
         for row, lo, hi, k in self.spans:
             h, H, E = init[k], init[k].abs(), torch.zeros_like(init[k])
             for t in range(lo, hi):
                 a = self.a[row, t]
                 self.before[row, t], self.ebefore[row, t] = h, E + 16 * U * H
-                E = a * E + (self.da[row, t] + 4 * U) * a * H + self.db * bt[row, t].abs()
+                E = a * E + (self.da[row, t] + 4 * U) * a * H + self.db * bt[row, t].abs() + m0[row, t]
                 h, H = a * h + bt[row, t], a * H + bt[row, t].abs()
                 E = E + 2 * U * H
                 self.h[row, t], self.eh[row, t] = h, E + 16 * U * H
             self.final[k], self.efinal[k] = h, E + (16 * U * H if hi > lo else 0)
         self.chunks, self.echunks = self.before[:, ::chunk], self.ebefore[:, ::chunk]
+        # The backward keeps 1 - a, rounded to half a step of 1, so there a is off by U (not U a) more, and so are
+        # the states that it recomputes from the chunk states: da_b and eb take the place of da a and ebefore.
+        self.da_b = self.da * self.a + 2 * U
+        self.eb = torch.zeros_like(x)
+        for row, lo, hi, k in self.spans:
+            H, E = init[k].abs(), torch.zeros_like(init[k])
+            for t in range(lo, hi):
+                self.eb[row, t] = E + 16 * U * H
+                a = self.a[row, t]
+                E = a * E + (self.da_b[row, t] + 4 * U * a) * H + self.db * bt[row, t].abs() + m0[row, t]
+                H = a * H + bt[row, t].abs()
+                E = E + 2 * U * H
 
     def grad(self, dy, dfinal=None):
         """{name: (value, bound)}"""
@@ -89,18 +105,19 @@ class Glr:
                 g[row, t], G = dy[row, t] + c, dy[row, t].abs() + C
                 eg[row, t] = E + 16 * U * G
                 c, C = a[row, t] * g[row, t], a[row, t] * G
-                E = a[row, t] * (E + 2 * U * G) + (self.da[row, t] + 4 * U) * C
+                E = a[row, t] * (E + 2 * U * G) + (self.da_b[row, t] + 4 * U * a[row, t]) * G
             dinit[k], edinit[k] = c, E + (16 * U * C if hi > lo else 0)
         ag, ax = g.abs(), x.abs()
         k1 = torch.where(m > 0, q * a * a / m.clamp(min=1e-300), torch.zeros_like(m)) * si * ax
         k2 = q * a
         dqq = torch.where(m > 0, q * a * a / m.clamp(min=1e-300), torch.zeros_like(m)) * si * x * g - k2 * g * self.before
-        e = k1 * (eg + ag * (3 * self.dq + 2 * self.da + self.ds + 32 * U))
-        e = e + k2 * (eg * self.before.abs() + ag * self.ebefore
-                      + ag * self.before.abs() * (self.dq + self.da + 16 * U))
+        e = k1 * (eg + ag * (3 * self.dq + self.ds + 32 * U))
+        e = e + k1 / a.clamp(min=1e-300) * ag * 2 * self.da_b              # a^2: 2 da_b a
+        e = e + k2 * (eg * self.before.abs() + ag * self.eb + ag * self.before.abs() * (self.dq + 16 * U))
+        e = e + q * self.da_b * ag * self.before.abs()
         return {
-            "dx": (g * m * si, m * si * (eg + ag * (self.db + 8 * U))),
-            "di": (g * m * x * si * self.osi, m * si * self.osi * ax * (eg + ag * (self.db + self.ds + 16 * U))),
+            "dx": (g * m * si, m * si * (eg + ag * (self.db + 8 * U)) + 2 * M0 * si * ag),
+            "di": (g * m * x * si * self.osi, (m * (eg + ag * (self.db + self.ds + 16 * U)) + 2 * M0 * ag) * si * self.osi * ax),
             "dr": (dqq * self.osr, self.osr * (e + dqq.abs() * (self.ds + 8 * U))),
             "dA_log": (dqq.sum((0, 1)), (e + 256 * U * dqq.abs()).sum((0, 1))),
             "dinitial_states": (dinit, edinit),
