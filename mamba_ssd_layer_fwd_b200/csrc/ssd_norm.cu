@@ -346,29 +346,34 @@ norm_bwd_team_kernel(NormArgs a, int lanes, int ncols, G *__restrict__ dx, G *__
         }
 }
 
-// A CTA keeps one group's columns and walks rows.  RING: thread 0 copies rows
-// `nst` ahead into shared memory (rows aligned to 16 bytes), so HBM reads go on
-// through the row's reduction; otherwise threads load their own columns.  The
-// weights are read again for each row, from L1: registers are for the sums.
-constexpr int kStages = 3;
+// A CTA keeps one group's columns and walks rows, R at a time: their sums meet
+// at one barrier.  RING: thread 0 copies rows `nst` ahead into shared memory
+// (rows aligned to 16 bytes), so HBM reads go on through the reduction;
+// otherwise threads load their own columns.  The weights stay in registers
+// where a thread has eight elements, and are read again for each row, from L1,
+// where it has sixteen.
+constexpr int kMaxStages = 6;
 
-template <typename T, typename G, int V, int NV, bool GATE, bool RING, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB)
+template <typename T, typename G, int V, int NV, int R, bool GATE, bool RING, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1)
 norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz, float *__restrict__ part)
 {
     extern __shared__ __align__(128) char ring[];
-    __shared__ float2 red[2][32];
-    __shared__ uint64_t full[kStages];
+    __shared__ float2 red[2][R][32];
+    __shared__ uint64_t full[kMaxStages];
     __shared__ int abort_wait;
+    constexpr bool KEEP = V * NV <= 8;
     const int t = threadIdx.x, n = blockDim.x, lane = t & 31, wp = t >> 5, nw = n >> 5;
     const int g = blockIdx.x % a.G, split = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
     const float inv = 1.0f / a.P;
     const bool has_res = !GATE && a.dres != nullptr;
     const int row_t = a.P * (int)sizeof(T), row_g = has_res ? a.P * (int)sizeof(G) : 0;
     const int stage_bytes = (GATE ? 3 : 2) * row_t + row_g;
-    const auto send = [&](long long row, int stage) {
+    const int count = split < a.rows ? (int)((a.rows - split + nsplit - 1) / nsplit) : 0;     // rows of this CTA
+    const auto send = [&](int q) {                  // the CTA's q-th row
+        const int stage = q % nst;
         char *to = ring + (size_t)stage * stage_bytes;
-        const long long at = row * a.D + c0;
+        const long long row = split + (long long)q * nsplit, at = row * a.D + c0;
         tc::mbar_arrive_expect_tx(&full[stage], stage_bytes);
         tc::bulk_load(to, static_cast<const T *>(a.x) + row * a.xs + c0, row_t, &full[stage]);
         tc::bulk_load(to + row_t, static_cast<const T *>(a.dy) + at, row_t, &full[stage]);
@@ -377,87 +382,116 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
     };
     if (RING && t == 0) {
         abort_wait = 0;
-        for (int k = 0; k < kStages; ++k) tc::mbar_init(&full[k], 1);
+        for (int k = 0; k < nst; ++k) tc::mbar_init(&full[k], 1);
         tc::mbar_fence_init();
-        for (int k = 0; k < nst; ++k)
-            if (split + (long long)k * nsplit < a.rows) send(split + (long long)k * nsplit, k);
+        for (int q = 0; q < min(nst, count); ++q) send(q);
     }
-    float dw[NV][V], db[NV][V];
+    float dw[NV][V], db[NV][V], w[KEEP ? NV : 1][V];
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
+    for (int k = 0; k < NV; ++k) {
+        const int c = (t + k * n) * V;
 #pragma unroll
-        for (int v = 0; v < V; ++v) dw[k][v] = db[k][v] = 0.0f;
+        for (int v = 0; v < V; ++v) dw[k][v] = db[k][v] = w[KEEP ? k : 0][v] = 0.0f;
+        if (KEEP && c < a.P) load_values<float, V>(a.w + c0 + c, w[k]);
+    }
     __syncthreads();
-    float mu_next = 0.0f, rs_next = 0.0f;
-    if (split < a.rows) mu_next = a.mean[(long long)split * a.G + g], rs_next = a.rstd[(long long)split * a.G + g];
+    float mu_next[R], rs_next[R];
+    const auto stats = [&](int q, float &mu, float &rs) {
+        mu = rs = 0.0f;
+        if (q < count) {
+            const long long at = (split + (long long)q * nsplit) * a.G + g;
+            mu = a.mean[at], rs = a.rstd[at];
+        }
+    };
+#pragma unroll
+    for (int r = 0; r < R; ++r) stats(r, mu_next[r], rs_next[r]);
     int stage = 0, parity = 0, turn = 0;
-    for (long long row = split; row < a.rows; row += nsplit) {
-        const float mu = mu_next, rs = rs_next;
-        if (row + nsplit < a.rows) mu_next = a.mean[(row + nsplit) * a.G + g], rs_next = a.rstd[(row + nsplit) * a.G + g];
-        const long long at = row * a.D + c0;
-        const char *here = ring + (size_t)stage * stage_bytes;
-        // a copy that does not arrive (2 s) is not waited for again: the row is then read in place
-        const bool staged = RING && tc::mbar_wait(&full[stage], parity, &abort_wait);
-        const T *x = staged ? reinterpret_cast<const T *>(here) : static_cast<const T *>(a.x) + row * a.xs + c0;
-        const T *dy = staged ? reinterpret_cast<const T *>(here + row_t) : static_cast<const T *>(a.dy) + at;
-        const T *z = !GATE ? nullptr : staged ? reinterpret_cast<const T *>(here + 2 * row_t)
-                                              : static_cast<const T *>(a.z) + row * a.zs + c0;
-        const G *dres = !has_res ? nullptr : staged ? reinterpret_cast<const G *>(here + 2 * row_t)
-                                                    : static_cast<const G *>(a.dres) + at;
-        Pack<T, V> xr[NV], zr[GATE ? NV : 1], dr[NV];
-        Raw<G, V> res[GATE ? 1 : NV];
+    for (int q = 0; q < count; q += R) {
+        float mu[R], rs[R];
+        Pack<T, V> xr[R][NV], zr[R][GATE ? NV : 1], dr[R][NV];
+        Raw<G, V> res[R][GATE ? 1 : NV];
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (t + k * n) * V;
+        for (int r = 0; r < R; ++r) {
+            mu[r] = mu_next[r], rs[r] = rs_next[r];
+            stats(q + R + r, mu_next[r], rs_next[r]);
+            const bool there = q + r < count;
+            const long long row = split + (long long)(q + r) * nsplit, at = row * a.D + c0;
+            const char *here = ring + (size_t)stage * stage_bytes;
+            // a copy that does not arrive (2 s) is not waited for again: the row is then read in place
+            const bool staged = RING && there && tc::mbar_wait(&full[stage], parity, &abort_wait);
+            const T *x = staged ? reinterpret_cast<const T *>(here) : static_cast<const T *>(a.x) + row * a.xs + c0;
+            const T *dy = staged ? reinterpret_cast<const T *>(here + row_t) : static_cast<const T *>(a.dy) + at;
+            const T *z = !GATE ? nullptr : staged ? reinterpret_cast<const T *>(here + 2 * row_t)
+                                                  : static_cast<const T *>(a.z) + row * a.zs + c0;
+            const G *dres = !has_res ? nullptr : staged ? reinterpret_cast<const G *>(here + 2 * row_t)
+                                                        : static_cast<const G *>(a.dres) + at;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (c >= a.P) xr[k].v[v] = dr[k].v[v] = zr[GATE ? k : 0].v[v] = from_f32<T>(0.0f);
-            if (c < a.P) {
-                xr[k] = load_pack<T, V>(x + c);
-                dr[k] = load_pack<T, V>(dy + c);
-                if (GATE) zr[k] = load_pack<T, V>(z + c);
-                if (!GATE && has_res) res[k].load(dres + c);
+            for (int k = 0; k < NV; ++k) {
+                const int c = (t + k * n) * V;
+                if (there && c < a.P) {
+                    xr[r][k] = load_pack<T, V>(x + c);
+                    dr[r][k] = load_pack<T, V>(dy + c);
+                    if (GATE) zr[r][k] = load_pack<T, V>(z + c);
+                    if (!GATE && has_res) res[r][k].load(dres + c);
+                } else {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) xr[r][k].v[v] = dr[r][k].v[v] = zr[r][GATE ? k : 0].v[v] = from_f32<T>(0.0f);
+                }
             }
+            if (++stage == nst) stage = 0, parity ^= 1;
         }
-        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            Cols<V> cl;
-            const int c = (t + k * n) * V;
-            float w[V];
+        for (int r = 0; r < R; ++r) {
+            float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-            for (int v = 0; v < V; ++v) w[v] = 0.0f;
-            if (c < a.P) load_values<float, V>(a.w + c0 + c, w);
-            columns<T, V, GATE>(xr[k], zr[GATE ? k : 0], dr[k], w, mu, rs, cl);
+            for (int k = 0; k < NV; ++k) {
+                Cols<V> cl;
+                const int c = (t + k * n) * V;
+                float wk[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s1 += cl.wd[v];
-                s2 = fmaf(cl.wd[v], cl.xh[v], s2);
-                dw[k][v] = fmaf(cl.dy[v], cl.xh[v], dw[k][v]);
-                db[k][v] += cl.dy[v];
+                for (int v = 0; v < V; ++v) wk[v] = KEEP ? w[KEEP ? k : 0][v] : 0.0f;
+                if (!KEEP && c < a.P) load_values<float, V>(a.w + c0 + c, wk);
+                columns<T, V, GATE>(xr[r][k], zr[r][GATE ? k : 0], dr[r][k], wk, mu[r], rs[r], cl);
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+                    s1 += cl.wd[v];
+                    s2 = fmaf(cl.wd[v], cl.xh[v], s2);
+                    dw[k][v] = fmaf(cl.dy[v], cl.xh[v], dw[k][v]);
+                    db[k][v] += cl.dy[v];
+                }
             }
+            s1 = team_sum(s1, 32);
+            s2 = team_sum(s2, 32);
+            if (lane == 0) red[turn][r][wp] = make_float2(s1, s2);
         }
-        s1 = team_sum(s1, 32);
-        s2 = team_sum(s2, 32);
-        if (lane == 0) red[turn][wp] = make_float2(s1, s2);
-        __syncthreads();                            // the row is in registers: its stage is free
-        if (RING && t == 0 && row + (long long)nst * nsplit < a.rows) send(row + (long long)nst * nsplit, stage);
-        s1 = s2 = 0.0f;
-        if (lane < nw) s1 = red[turn][lane].x, s2 = red[turn][lane].y;
-        s1 = team_sum(s1, 32) * inv;
-        s2 = team_sum(s2, 32) * inv;
+        __syncthreads();                            // the rows are in registers: their stages are free
+        if (RING && t == 0)
+            for (int r = 0; r < R; ++r)
+                if (q + r + nst < count) send(q + r + nst);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (t + k * n) * V;
-            if (c >= a.P) break;
-            Cols<V> cl;
-            float w[V];
-            load_values<float, V>(a.w + c0 + c, w);
-            columns<T, V, GATE>(xr[k], zr[GATE ? k : 0], dr[k], w, mu, rs, cl);
-            write_columns<G, V, GATE>(cl, rs, s1, s2, has_res, res[GATE ? 0 : k], dx + at + c, GATE ? dz + at + c : nullptr);
+        for (int r = 0; r < R; ++r) {
+            if (q + r >= count) break;
+            float2 s = make_float2(0.0f, 0.0f);
+            if (lane < nw) s = red[turn][r][lane];
+            const float s1 = team_sum(s.x, 32) * inv, s2 = team_sum(s.y, 32) * inv;
+            const long long at = (split + (long long)(q + r) * nsplit) * a.D + c0;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (t + k * n) * V;
+                if (c >= a.P) break;
+                Cols<V> cl;
+                float wk[V];
+                if (KEEP) {
+#pragma unroll
+                    for (int v = 0; v < V; ++v) wk[v] = w[KEEP ? k : 0][v];
+                } else {
+                    load_values<float, V>(a.w + c0 + c, wk);
+                }
+                columns<T, V, GATE>(xr[r][k], zr[r][GATE ? k : 0], dr[r][k], wk, mu[r], rs[r], cl);
+                write_columns<G, V, GATE>(cl, rs[r], s1, s2, has_res, res[r][GATE ? 0 : k], dx + at + c, GATE ? dz + at + c : nullptr);
+            }
         }
         turn ^= 1;
-        if (++stage == nst) stage = 0, parity ^= 1;
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -602,19 +636,24 @@ void fwd(const NormArgs &a, void *y, void *sum, float *mean, float *rstd, cudaSt
     else fwd_mode<T, V, kPlain>(a, y, sum, mean, rstd, st);
 }
 
-// Vectors a thread of the backward's CTA.
-int vectors_of(int vecs, int V)
-{
-    if (V == 1) return vecs <= 1536 ? 4 : 16;
-    return vecs <= 384 ? 1 : vecs <= 768 || V == 8 ? 2 : 16 / V;
-}
+// The backward's CTA: eight elements a thread and two rows at a time up to 768
+// threads (80 registers; one row with a gate), then sixteen and one row.
+constexpr int kCtaThreads = 768;
+int vectors_of(int vecs, int V) { return (vecs * V <= 8 * kCtaThreads ? 8 : 16) / V; }
 
 // How the backward splits a call; the same for any alignment, so that the
 // workspace can be sized before it is known.
 struct Split {
     bool team;
-    int lanes, ncols, nsplit;
+    int lanes, ncols, nsplit, per_sm;
 };
+
+// CTAs that fit an SM's registers, 80 a thread (64 to 128 in CTAs of sixteen elements a thread: one).
+int ctas_per_sm(int P, int V)
+{
+    const int vecs = (P + V - 1) / V, nv = vectors_of(vecs, V);
+    return nv * V == 8 ? std::max(1, std::min(8, 65536 / (80 * threads_of(vecs, nv)))) : 1;
+}
 
 Split split_of(const ssd_layer_norm_params &p, int V)
 {
@@ -628,11 +667,9 @@ Split split_of(const ssd_layer_norm_params &p, int V)
         const int64_t most = (rows + kTeamThreads / 32 - 1) / (kTeamThreads / 32);
         s.nsplit = (int)std::min<int64_t>(most, std::max(1, sm_count() * 4 / s.ncols));
     } else {
-        // as many CTAs as fit the registers: 80 a thread up to 384 threads, 128 (64 above 512 threads) otherwise
-        const int vecs = (P + V - 1) / V, t = threads_of(vecs, vectors_of(vecs, V));
-        const int per_sm = t <= 384 ? std::min(8, 65536 / (80 * t)) : 1;
+        s.per_sm = ctas_per_sm(P, V);
         s.ncols = p.ngroups;
-        s.nsplit = (int)std::min<int64_t>(rows, std::max(1, (sm_count() * per_sm + s.ncols - 1) / s.ncols));
+        s.nsplit = (int)std::min<int64_t>(rows, std::max(1, (sm_count() * s.per_sm + s.ncols - 1) / s.ncols));
     }
     return s;
 }
@@ -650,16 +687,17 @@ cudaError_t bwd_team(const NormArgs &a, const Split &s, const BwdOut &o, cudaStr
     return cudaGetLastError();
 }
 
-template <typename T, typename G, int V, int NV, bool GATE, int MAXT, int MINB>
+template <typename T, typename G, int V, int NV, int R, bool GATE, int MAXT>
 cudaError_t bwd_cta(const NormArgs &a, const Split &s, const BwdOut &o, cudaStream_t st)
 {
     constexpr bool RING = V > 1;
-    const auto kernel = norm_bwd_cta_kernel<T, G, V, NV, GATE, RING, MAXT, MINB>;
+    const auto kernel = norm_bwd_cta_kernel<T, G, V, NV, R, GATE, RING, MAXT>;
     size_t smem = 0;
-    int nst = 0;
+    int nst = 1;
     if (RING) {
+        // R stages at least: with 16 elements a thread the longest group's one has 192 KB, with 8 three have 216 KB
         const size_t stage = (size_t)a.P * ((GATE ? 3 : 2) * sizeof(T) + (a.dres ? sizeof(G) : 0));
-        nst = (int)std::min<size_t>(kStages, (size_t)220 * 1024 / stage);      // one stage of the longest group: 192 KB
+        nst = (int)std::min<size_t>(kMaxStages, std::max<size_t>(R, (size_t)216 * 1024 / s.per_sm / stage));
         smem = nst * stage;
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
@@ -678,25 +716,16 @@ cudaError_t bwd_gate(const NormArgs &a, const Split &s, const BwdOut &o, cudaStr
             if (a.P <= 32) return bwd_team<T, G, 1, 1, GATE>(a, s, o, st);
             return a.P <= 128 ? bwd_team<T, G, 1, 4, GATE>(a, s, o, st) : bwd_team<T, G, 1, 8, GATE>(a, s, o, st);
         }
-        if (vectors_of(vecs, V) == 4) return bwd_cta<T, G, 1, 4, GATE, 384, 2>(a, s, o, st);
-        if (vecs <= 6144) return bwd_cta<T, G, 1, 16, GATE, 384, 2>(a, s, o, st);
-        if (vecs <= 8192) return bwd_cta<T, G, 1, 16, GATE, 512, 1>(a, s, o, st);
-        return bwd_cta<T, G, 1, 16, GATE, 1024, 1>(a, s, o, st);
     } else {
         if (s.team) {
             if (vecs <= 32) return bwd_team<T, G, V, 1, GATE>(a, s, o, st);
             if (vecs <= 64) return bwd_team<T, G, V, 2, GATE>(a, s, o, st);
             if constexpr (V == 4) return bwd_team<T, G, V, 4, GATE>(a, s, o, st);
         }
-        constexpr int S = 16 / V;
-        const int nv = vectors_of(vecs, V), t = threads_of(vecs, nv);
-        if (nv == 1) return bwd_cta<T, G, V, 1, GATE, 384, 2>(a, s, o, st);
-        if constexpr (S > 2)
-            if (nv == 2) return bwd_cta<T, G, V, 2, GATE, 384, 2>(a, s, o, st);
-        if (t <= 384) return bwd_cta<T, G, V, S, GATE, 384, 2>(a, s, o, st);
-        if (t <= 512) return bwd_cta<T, G, V, S, GATE, 512, 1>(a, s, o, st);
-        return bwd_cta<T, G, V, S, GATE, 1024, 1>(a, s, o, st);
     }
+    if (vectors_of(vecs, V) * V == 8) return bwd_cta<T, G, V, 8 / V, GATE ? 1 : 2, GATE, kCtaThreads>(a, s, o, st);
+    if (vecs * V <= 8192) return bwd_cta<T, G, V, 16 / V, 1, GATE, 512>(a, s, o, st);
+    return bwd_cta<T, G, V, 16 / V, 1, GATE, 1024>(a, s, o, st);
 }
 
 template <typename T, typename G, int V>
