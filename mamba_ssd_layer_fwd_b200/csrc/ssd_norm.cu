@@ -18,6 +18,7 @@
 
 #include "ssd_common.cuh"
 #include "ssd_norm.h"
+#include "ssd_pairs.cuh"
 #include "ssd_tc_prims.cuh"
 
 namespace ssd {
@@ -37,61 +38,77 @@ enum Mode { kPlain, kResidual, kGate };
 template <typename T, int V> struct alignas(sizeof(T) * V) Pack {
     T v[V];
 };
-template <typename T, int V>
-__device__ __forceinline__ void unpack(const Pack<T, V> &p, float (&f)[V])
-{
-#pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = to_f32(p.v[k]);
-}
-template <typename T, int V>
-__device__ __forceinline__ Pack<T, V> load_pack(const T *p)
-{
-    return *reinterpret_cast<const Pack<T, V> *>(p);
-}
-// V values at an address aligned to min(16 bytes, all of them)
-template <typename T, int V>
-__device__ __forceinline__ void store_values(T *p, const float (&f)[V])
-{
-    constexpr int N = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
-#pragma unroll
-    for (int k = 0; k < V; k += N) {
-        Pack<T, N> o;
-#pragma unroll
-        for (int q = 0; q < N; ++q) o.v[q] = from_f32<T>(f[k + q]);
-        *reinterpret_cast<Pack<T, N> *>(p + k) = o;
-    }
-}
-template <typename T, int V>
-__device__ __forceinline__ void load_values(const T *p, float (&f)[V])
-{
-    constexpr int N = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
-#pragma unroll
-    for (int k = 0; k < V; k += N) {
-        const Pack<T, N> o = load_pack<T, N>(p + k);
-#pragma unroll
-        for (int q = 0; q < N; ++q) f[k + q] = to_f32(o.v[q]);
-    }
-}
 
-// V values of type T as they lie in memory
-template <typename T, int V> struct Raw {
-    static constexpr int N = V * (int)sizeof(T) > 16 ? 16 / (int)sizeof(T) : V;
-    Pack<T, N> p[V / N];
-    __device__ __forceinline__ void load(const T *from)
+// A thread's NV vectors of V elements, as they lie in memory and as E / 2 pairs
+// of float32 (V = 1: two vectors a pair).
+template <typename T, int V, int NV> struct Raw {
+    static constexpr int E = V * NV;
+    Pack<T, V> v[NV];
+    __device__ __forceinline__ void load(int k, const T *p) { v[k] = *reinterpret_cast<const Pack<T, V> *>(p); }
+    __device__ __forceinline__ void zero(int k)
     {
 #pragma unroll
-        for (int k = 0; k < V / N; ++k) p[k] = load_pack<T, N>(from + k * N);
+        for (int q = 0; q < V; ++q) v[k].v[q] = from_f32<T>(0.0f);
     }
-    __device__ __forceinline__ float value(int v) const { return to_f32(p[v / N].v[v % N]); }
+    __device__ __forceinline__ F2 pair(int i) const
+    {
+        if constexpr (V == 1) {
+            return f2(to_f32(v[2 * i].v[0]), to_f32(v[2 * i + 1].v[0]));
+        } else if constexpr (sizeof(T) == 4) {
+            return f2(v[2 * i / V].v[2 * i % V], v[2 * i / V].v[2 * i % V + 1]);
+        } else {
+            const uint32_t w = reinterpret_cast<const uint32_t *>(&v[2 * i / V])[i % (V / 2)];
+            return f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+        }
+    }
 };
 
-__device__ __forceinline__ float rcp_fast(float v)
+// The k-th vector's V values of `f` (E / 2 pairs) to p, in 16-byte pieces where V > 1.
+template <typename T, int V, int H>
+__device__ __forceinline__ void store_vector(T *p, int k, const F2 (&f)[H])
 {
-    float o;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
-    return o;
+    if constexpr (V == 1) {
+        float x, y;
+        split(f[k / 2], x, y);
+        *p = from_f32<T>(k % 2 ? y : x);
+    } else if constexpr (sizeof(T) == 2) {
+        const int i = k * V / 2;
+        *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16(f[i]), pack_bf16(f[i + 1]), pack_bf16(f[i + 2]), pack_bf16(f[i + 3]));
+    } else {
+#pragma unroll
+        for (int q = 0; q < V / 4; ++q) {
+            float4 o;
+            split(f[(k * V + 4 * q) / 2], o.x, o.y), split(f[(k * V + 4 * q) / 2 + 1], o.z, o.w);
+            *reinterpret_cast<float4 *>(p + 4 * q) = o;
+        }
+    }
 }
-__device__ __forceinline__ float sigmoid(float z) { return rcp_fast(1.0f + tc::ex2_approx(z * -1.4426950408889634f)); }
+
+// Gradients' values may be wider than x's: V of them in pieces of 16 bytes.
+template <typename G, int V, int NV> struct RawGrad {
+    static constexpr int N = V * (int)sizeof(G) > 16 ? 16 / (int)sizeof(G) : V;
+    Raw<G, N, NV * V / N> r;
+    __device__ __forceinline__ void load(int k, const G *p)
+    {
+#pragma unroll
+        for (int q = 0; q < V / N; ++q) r.load(k * (V / N) + q, p + q * N);
+    }
+    __device__ __forceinline__ F2 pair(int i) const { return r.pair(i); }
+};
+
+__device__ __forceinline__ float total(F2 a)
+{
+    float x, y;
+    split(a, x, y);
+    return x + y;
+}
+__device__ __forceinline__ F2 negated(float v) { return f2(-v); }
+
+__device__ __forceinline__ F2 sigmoid2(F2 z)
+{
+    const F2 e = each(mul(z, f2(-1.4426950408889634f)), [](float v) { return ex2_approx(v); });
+    return each(add(e, f2(1.0f)), [](float v) { return rcp_approx(v); });
+}
 
 // Sum over `lanes` (a power of two) neighbouring lanes, in all of them.
 __device__ __forceinline__ float team_sum(float v, int lanes)
@@ -114,236 +131,366 @@ __device__ __forceinline__ float cta_sum(float v, float *slots)
 
 // ---------------------------------------------------------------- forward
 
-// One unit (a group of a row): lane `t` of its team of n holds the vectors t,
-// t + n, ... of V channels.  Sum is a callable that adds a value over the team.
-template <typename T, int V, int NV, Mode M, typename Sum>
-__device__ __forceinline__ void norm_unit(const NormArgs &a, long long row, int g, int t, int n, bool live, T *y, T *sum,
-                                          float *mean, float *rstd, Sum team)
-{
-    const int c0 = g * a.P;
-    const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
-    const T *z = M == kGate ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
-    const long long at = row * a.D + c0;
-    Pack<T, V> xr[NV], zr[M == kPlain ? 1 : NV];
+// A thread's part of one row: vectors t, t + n, ... of the group that starts at
+// channel c0.
+template <typename T, int V, int NV, Mode M> struct FwdRow {
+    static constexpr int H = V * NV / 2;
+    Raw<T, V, NV> x;
+    Raw<T, V, M == kPlain ? 2 : NV> z;
+    F2 u[H];
+
+    __device__ __forceinline__ void load(const NormArgs &a, long long row, int c0, int t, int n, bool live)
+    {
+        const T *xp = static_cast<const T *>(a.x) + row * a.xs + c0;
+        const T *zp = M == kGate       ? static_cast<const T *>(a.z) + row * a.zs + c0
+                      : M == kResidual ? static_cast<const T *>(a.res) + row * a.D + c0
+                                       : nullptr;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (t + k * n) * V;
-        if (live && c < a.P) {
-            xr[k] = load_pack<T, V>(x + c);
-            if (M == kGate) zr[k] = load_pack<T, V>(z + c);
-            if (M == kResidual) zr[k] = load_pack<T, V>(static_cast<const T *>(a.res) + at + c);
-        }
-    }
-    float u[NV][V], s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (t + k * n) * V;
-        const bool in = live && c < a.P;
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            float f = 0.0f;
-            if (in) {
-                f = to_f32(xr[k].v[v]);
-                if (M == kGate) {
-                    const float zv = to_f32(zr[k].v[v]);
-                    f *= zv * sigmoid(zv);
-                }
-                if (M == kResidual) f = to_f32(from_f32<T>(f + to_f32(zr[k].v[v])));
+        for (int k = 0; k < NV; ++k) {
+            const int c = (t + k * n) * V;
+            if (live && c < a.P) {
+                x.load(k, xp + c);
+                if (M != kPlain) z.load(k, zp + c);
+            } else {
+                x.zero(k);
+                if (M != kPlain) z.zero(k);
             }
-            u[k][v] = o[v] = f;
-            s += f;
-        }
-        if (M == kResidual && in) store_values<T, V>(sum + at + c, o);
-    }
-    const float inv = 1.0f / a.P;
-    s = team(s);
-    float mu = s * inv;
-    mu = fmaf(fmaf(-mu, (float)a.P, s), inv, mu);   // s / P rounded once: a row of one value has no spread
-    s = 0.0f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const bool in = live && (t + k * n) * V < a.P;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            u[k][v] -= mu;
-            if (in) s = fmaf(u[k][v], u[k][v], s);
         }
     }
-    const float rs = rsqrtf(fmaf(team(s), inv, a.eps));
-    if (!live) return;
-    if (t == 0) {
-        if (mean) mean[row * a.G + g] = mu;
-        if (rstd) rstd[row * a.G + g] = rs;
+
+    // u, its sum over the thread's elements; writes the residual's sum
+    __device__ __forceinline__ float input(const NormArgs &a, long long row, int c0, int t, int n, bool live, T *sum)
+    {
+        F2 s = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            F2 v = x.pair(i);
+            if constexpr (M == kGate) {
+                const F2 zv = z.pair(i);
+                v = mul(v, mul(zv, sigmoid2(zv)));
+            }
+            if constexpr (M == kResidual) {
+                v = add(v, z.pair(i));
+                if constexpr (sizeof(T) == 2) {
+                    const uint32_t w = pack_bf16(v);        // what is normalised is the sum that is kept
+                    v = f2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                }
+            }
+            u[i] = v;
+            s = add(s, v);
+        }
+        if constexpr (M == kResidual) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = (t + k * n) * V;
+                if (live && c < a.P) store_vector<T, V>(sum + row * a.D + c0 + c, k, u);
+            }
+        }
+        return total(s);
     }
+
+    // u - mu, the sum of its squares
+    __device__ __forceinline__ float centre(const NormArgs &a, float mu, int t, int n)
+    {
+        F2 s = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            u[i] = add(u[i], negated(mu));
+            if constexpr (V > 1) {
+                if ((t + 2 * i / V * n) * V < a.P) s = fma(u[i], u[i], s);
+            } else {
+                float x, y;
+                split(u[i], x, y);
+                if (t + (2 * i + 1) * n >= a.P) y = 0.0f;
+                if (t + 2 * i * n >= a.P) x = 0.0f;
+                s = fma(f2(x, y), f2(x, y), s);
+            }
+        }
+        return total(s);
+    }
+
+    __device__ __forceinline__ void write(const NormArgs &a, long long row, int g, int t, int n, bool live, float mu,
+                                          float rs, const F2 (&w)[H], const F2 (&b)[H], T *y, float *mean, float *rstd)
+    {
+        if (!live) return;
+        if (t == 0) {
+            if (mean) mean[row * a.G + g] = mu;
+            if (rstd) rstd[row * a.G + g] = rs;
+        }
+#pragma unroll
+        for (int i = 0; i < H; ++i) u[i] = fma(mul(u[i], f2(rs)), w[i], b[i]);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (t + k * n) * V;
+            if (c < a.P) store_vector<T, V>(y + row * a.D + (long long)g * a.P + c, k, u);
+        }
+    }
+};
+
+// s / P rounded once, so that a row of one value has no spread
+__device__ __forceinline__ float mean_of(float s, int P, float inv)
+{
+    const float mu = s * inv;
+    return fmaf(fmaf(-mu, (float)P, s), inv, mu);
+}
+
+// float32 parameters of a thread's columns (zeros where there are none)
+template <int V, int NV>
+__device__ __forceinline__ void load_params(const float *p, int P, int t, int n, F2 (&f)[V * NV / 2])
+{
+    float v[V * NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
         const int c = (t + k * n) * V;
-        if (c >= a.P) break;
-        float w[V], b[V], o[V];
-        load_values<float, V>(a.w + c0 + c, w);
-        if (a.b) load_values<float, V>(a.b + c0 + c, b);
+        const bool in = p && c < P;
 #pragma unroll
-        for (int v = 0; v < V; ++v) o[v] = fmaf(u[k][v] * rs, w[v], a.b ? b[v] : 0.0f);
-        store_values<T, V>(y + at + c, o);
+        for (int q = 0; q < V; q += 4) {
+            if constexpr (V == 1) {
+                v[k] = in ? p[c] : 0.0f;
+            } else {
+                const float4 o = in ? *reinterpret_cast<const float4 *>(p + c + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[k * V + q] = o.x, v[k * V + q + 1] = o.y, v[k * V + q + 2] = o.z, v[k * V + q + 3] = o.w;
+            }
+        }
     }
+#pragma unroll
+    for (int i = 0; i < V * NV / 2; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 constexpr int kTeamThreads = 256;
 
-// lanes: 8, 16 or 32 with lanes V NV >= P
-template <typename T, int V, int NV, Mode M>
-__global__ void __launch_bounds__(kTeamThreads)
-norm_fwd_team_kernel(NormArgs a, int lanes, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean,
+// A warp has 32 / lanes neighbouring groups of a row (lanes: 8, 16 or 32 with
+// lanes V NV >= P) and walks rows, R at a time.
+template <typename T, int V, int NV, int R, Mode M>
+__global__ void __launch_bounds__(kTeamThreads, 2)
+norm_fwd_team_kernel(NormArgs a, int lanes, int ncols, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean,
                      float *__restrict__ rstd)
 {
-    const unsigned unit = blockIdx.x * (kTeamThreads / lanes) + threadIdx.x / lanes;
-    const unsigned row = unit / a.G;
-    norm_unit<T, V, NV, M>(a, row, unit - row * a.G, threadIdx.x & (lanes - 1), lanes, row < a.rows, y, sum, mean, rstd,
-                           [&](float v) { return team_sum(v, lanes); });
+    constexpr int W = kTeamThreads / 32, H = V * NV / 2;
+    const int lane = threadIdx.x & 31, t = lane & (lanes - 1);
+    const int col = blockIdx.x % ncols;
+    const int g = col * (32 / lanes) + lane / lanes, c0 = g * a.P;
+    const long long first = (long long)(blockIdx.x / ncols) * W + (threadIdx.x >> 5), step = (long long)(gridDim.x / ncols) * W;
+    const bool live = g < a.G;
+    const float inv = 1.0f / a.P;
+    F2 w[H], b[H];
+    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, w);
+    load_params<V, NV>(live && a.b ? a.b + c0 : nullptr, a.P, t, lanes, b);
+    for (long long row = first; row < a.rows; row += R * step) {
+        FwdRow<T, V, NV, M> r[R];
+        float s[R], mu[R];
+#pragma unroll
+        for (int k = 0; k < R; ++k) r[k].load(a, row + k * step, c0, t, lanes, live && row + k * step < a.rows);
+#pragma unroll
+        for (int k = 0; k < R; ++k) s[k] = r[k].input(a, row + k * step, c0, t, lanes, live && row + k * step < a.rows, sum);
+#pragma unroll
+        for (int k = 0; k < R; ++k) mu[k] = mean_of(team_sum(s[k], lanes), a.P, inv);
+#pragma unroll
+        for (int k = 0; k < R; ++k) s[k] = r[k].centre(a, mu[k], t, lanes);
+#pragma unroll
+        for (int k = 0; k < R; ++k)
+            r[k].write(a, row + k * step, g, t, lanes, live && row + k * step < a.rows, mu[k],
+                       rsqrtf(fmaf(team_sum(s[k], lanes), inv, a.eps)), w, b, y, mean, rstd);
+    }
 }
 
-template <typename T, int V, int NV, Mode M>
-__global__ void __launch_bounds__(1024)
+template <typename T, int V, int NV, Mode M, int MAXT>
+__global__ void __launch_bounds__(MAXT, 1)
 norm_fwd_cta_kernel(NormArgs a, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean, float *__restrict__ rstd)
 {
     __shared__ float slots[2][32];
-    int turn = 0;
+    constexpr int H = V * NV / 2;
     const unsigned unit = blockIdx.x, row = unit / a.G;
-    norm_unit<T, V, NV, M>(a, row, unit - row * a.G, threadIdx.x, blockDim.x, true, y, sum, mean, rstd,
-                           [&](float v) { return cta_sum(v, slots[turn++]); });
+    const int g = unit - row * a.G, t = threadIdx.x, n = blockDim.x, c0 = g * a.P;
+    const float inv = 1.0f / a.P;
+    FwdRow<T, V, NV, M> r;
+    r.load(a, row, c0, t, n, true);
+    F2 w[H], b[H];
+    load_params<V, NV>(a.w + c0, a.P, t, n, w);
+    load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
+    const float mu = mean_of(cta_sum(r.input(a, row, c0, t, n, true, sum), slots[0]), a.P, inv);
+    const float rs = rsqrtf(fmaf(cta_sum(r.centre(a, mu, t, n), slots[1]), inv, a.eps));
+    r.write(a, row, g, t, n, true, mu, rs, w, b, y, mean, rstd);
 }
 
 // ---------------------------------------------------------------- backward
 
-// A thread's V columns of one row.
-template <int V> struct Cols {
-    float xh[V], wd[V], dy[V];      // xhat, w dy, dy
-    float x[V], z[V], sz[V];        // gate: x, z, sigmoid(z)
+// A thread's part of one row.
+template <typename T, typename G, int V, int NV, bool GATE> struct BwdRow {
+    static constexpr int H = V * NV / 2;
+    Raw<T, V, NV> x, dy;
+    Raw<T, V, GATE ? NV : 2> z;
+    RawGrad<G, V, GATE ? 2 : NV> dres;
+    float mu, rs;
+
+    __device__ __forceinline__ void load(const T *xp, const T *dyp, const T *zp, const G *resp, int P, int t, int n, bool live)
+    {
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (t + k * n) * V;
+            if (live && c < P) {
+                x.load(k, xp + c);
+                dy.load(k, dyp + c);
+                if constexpr (GATE) z.load(k, zp + c);
+                else if (resp) dres.load(k, resp + c);
+            } else {
+                x.zero(k);
+                dy.zero(k);
+                if constexpr (GATE) z.zero(k);
+            }
+        }
+    }
+
+    // xhat and w dy of a pair of columns
+    __device__ __forceinline__ F2 hat(int i) const
+    {
+        F2 u = x.pair(i);
+        if constexpr (GATE) {
+            const F2 zv = z.pair(i);
+            u = mul(u, mul(zv, sigmoid2(zv)));
+        }
+        return mul(add(u, negated(mu)), f2(rs));
+    }
+
+    // sums of w dy and w dy xhat over the thread's elements; dw and db go on
+    __device__ __forceinline__ void sums(const F2 (&w)[H], F2 (&dw)[H], F2 (&db)[H], float &s1, float &s2) const
+    {
+        F2 a = f2(0.0f), b = f2(0.0f);
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            const F2 d = dy.pair(i), wd = mul(d, w[i]), xh = hat(i);
+            a = add(a, wd);
+            b = fma(wd, xh, b);
+            dw[i] = fma(d, xh, dw[i]);
+            db[i] = add(db[i], d);
+        }
+        s1 = total(a), s2 = total(b);
+    }
+
+    __device__ __forceinline__ void write(const F2 (&w)[H], float s1, float s2, bool has_res, int P, int t, int n, G *dx,
+                                          G *dz) const
+    {
+        F2 o[H], oz[GATE ? H : 1];
+#pragma unroll
+        for (int i = 0; i < H; ++i) {
+            F2 xv = x.pair(i), zv, sz, u = xv;
+            if constexpr (GATE) {
+                zv = z.pair(i), sz = sigmoid2(zv);
+                u = mul(xv, mul(zv, sz));
+            }
+            const F2 xh = mul(add(u, negated(mu)), f2(rs));
+            const F2 du = mul(fma(xh, f2(-s2), fma(dy.pair(i), w[i], f2(-s1))), f2(rs));
+            if constexpr (GATE) {
+                o[i] = mul(du, mul(zv, sz));
+                // silu' = s (1 + z (1 - s))
+                oz[i] = mul(mul(du, xv), mul(sz, fma(zv, fma(sz, f2(-1.0f), f2(1.0f)), f2(1.0f))));
+            } else {
+                o[i] = has_res ? add(du, dres.pair(i)) : du;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+            const int c = (t + k * n) * V;
+            if (c >= P) break;
+            store_vector<G, V>(dx + c, k, o);
+            if constexpr (GATE) store_vector<G, V>(dz + c, k, oz);
+        }
+    }
 };
 
-template <typename T, int V, bool GATE>
-__device__ __forceinline__ void columns(const Pack<T, V> &x, const Pack<T, V> &z, const Pack<T, V> &dy,
-                                        const float (&w)[V], float mu, float rs, Cols<V> &o)
-{
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        float u = to_f32(x.v[v]);
-        if (GATE) {
-            o.x[v] = u;
-            o.z[v] = to_f32(z.v[v]);
-            o.sz[v] = sigmoid(o.z[v]);
-            u *= o.z[v] * o.sz[v];
-        }
-        o.xh[v] = (u - mu) * rs;
-        o.dy[v] = to_f32(dy.v[v]);
-        o.wd[v] = o.dy[v] * w[v];
-    }
-}
-
-template <typename G, int V, bool GATE>
-__device__ __forceinline__ void write_columns(const Cols<V> &k, float rs, float s1, float s2, bool has_res,
-                                              const Raw<G, V> &dres, G *dx, G *dz)
-{
-    float o[V], oz[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-        const float du = rs * (k.wd[v] - s1 - k.xh[v] * s2);
-        if (GATE) {
-            o[v] = du * k.z[v] * k.sz[v];
-            oz[v] = du * k.x[v] * (k.sz[v] * fmaf(k.z[v], 1.0f - k.sz[v], 1.0f));
-        } else {
-            o[v] = has_res ? du + dres.value(v) : du;
-        }
-    }
-    store_values<G, V>(dx, o);
-    if (GATE) store_values<G, V>(dz, oz);
-}
-
-// Warps of a CTA share 32 / lanes neighbouring groups and take rows in turn.
-// part: [CTA of the columns][2][D].
-template <typename T, typename G, int V, int NV, bool GATE>
-__global__ void __launch_bounds__(kTeamThreads)
+// Warps of a CTA share 32 / lanes neighbouring groups and take rows in turn, R
+// at a time.  part: [CTA of the columns][2][D].
+template <typename T, typename G, int V, int NV, int R, bool GATE>
+__global__ void __launch_bounds__(kTeamThreads, 2)
 norm_bwd_team_kernel(NormArgs a, int lanes, int ncols, G *__restrict__ dx, G *__restrict__ dz, float *__restrict__ part)
 {
-    constexpr int W = kTeamThreads / 32;
-    __shared__ float red[W][32 * V];
+    constexpr int W = kTeamThreads / 32, H = V * NV / 2;
+    __shared__ float2 red[W][32];
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, t = lane & (lanes - 1);
-    const int col = blockIdx.x % ncols, split = blockIdx.x / ncols, nsplit = gridDim.x / ncols;
+    const int col = blockIdx.x % ncols, split_ = blockIdx.x / ncols;
+    const long long step = (long long)(gridDim.x / ncols) * W;
     const int g = col * (32 / lanes) + lane / lanes, c0 = g * a.P;
     const bool live = g < a.G;
     const float inv = 1.0f / a.P;
-    float w[NV][V], dw[NV][V], db[NV][V];
-    bool in[NV];
+    F2 w[H], dw[H], db[H];
+    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, w);
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (t + k * lanes) * V;
-        in[k] = live && c < a.P;
+    for (int i = 0; i < H; ++i) dw[i] = db[i] = f2(0.0f);
+    for (long long row0 = (long long)split_ * W + wp; row0 < a.rows; row0 += R * step) {
+        BwdRow<T, G, V, NV, GATE> r[R];
+        float s1[R], s2[R];
 #pragma unroll
-        for (int v = 0; v < V; ++v) w[k][v] = dw[k][v] = db[k][v] = 0.0f;
-        if (in[k]) load_values<float, V>(a.w + c0 + c, w[k]);
-    }
-    for (long long row = (long long)split * W + wp; row < a.rows; row += (long long)nsplit * W) {
-        const T *x = static_cast<const T *>(a.x) + row * a.xs + c0;
-        const T *z = GATE ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr;
-        const long long at = row * a.D + c0;
-        Pack<T, V> xr[NV], zr[GATE ? NV : 1], dr[NV];
-        Raw<G, V> res[GATE ? 1 : NV];
-        float mu = 0.0f, rs = 0.0f;
-        if (live) mu = a.mean[row * a.G + g], rs = a.rstd[row * a.G + g];
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (t + k * lanes) * V;
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (!in[k]) xr[k].v[v] = dr[k].v[v] = zr[GATE ? k : 0].v[v] = from_f32<T>(0.0f);
-            if (in[k]) {
-                xr[k] = load_pack<T, V>(x + c);
-                dr[k] = load_pack<T, V>(static_cast<const T *>(a.dy) + at + c);
-                if (GATE) zr[k] = load_pack<T, V>(z + c);
-                if (!GATE && a.dres) res[k].load(static_cast<const G *>(a.dres) + at + c);
-            }
+        for (int k = 0; k < R; ++k) {
+            const long long row = row0 + k * step, at = row * a.D + c0;
+            const bool there = live && row < a.rows;
+            r[k].mu = r[k].rs = 0.0f;
+            if (there) r[k].mu = a.mean[row * a.G + g], r[k].rs = a.rstd[row * a.G + g];
+            r[k].load(static_cast<const T *>(a.x) + row * a.xs + c0, static_cast<const T *>(a.dy) + at,
+                      GATE ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr,
+                      !GATE && a.dres ? static_cast<const G *>(a.dres) + at : nullptr, a.P, t, lanes, there);
         }
-        Cols<V> cl[NV];
-        float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            columns<T, V, GATE>(xr[k], zr[GATE ? k : 0], dr[k], w[k], mu, rs, cl[k]);
+        for (int k = 0; k < R; ++k) r[k].sums(w, dw, db, s1[k], s2[k]);
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                s1 += cl[k].wd[v];
-                s2 = fmaf(cl[k].wd[v], cl[k].xh[v], s2);
-                dw[k][v] = fmaf(cl[k].dy[v], cl[k].xh[v], dw[k][v]);
-                db[k][v] += cl[k].dy[v];
-            }
+        for (int k = 0; k < R; ++k) {
+            s1[k] = team_sum(s1[k], lanes) * inv;
+            s2[k] = team_sum(s2[k], lanes) * inv;
         }
-        s1 = team_sum(s1, lanes) * inv;
-        s2 = team_sum(s2, lanes) * inv;
 #pragma unroll
-        for (int k = 0; k < NV; ++k)
-            if (in[k]) {
-                const long long o = at + (t + k * lanes) * V;
-                write_columns<G, V, GATE>(cl[k], rs, s1, s2, a.dres != nullptr, res[GATE ? 0 : k], dx + o, GATE ? dz + o : nullptr);
-            }
+        for (int k = 0; k < R; ++k) {
+            const long long row = row0 + k * step, at = row * a.D + c0;
+            if (live && row < a.rows)
+                r[k].write(w, s1[k], s2[k], !GATE && a.dres, a.P, t, lanes, dx + at, GATE ? dz + at : nullptr);
+        }
     }
     // the warps' sums, in order
-    for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            __syncthreads();
+    for (int i = 0; i < 2 * H; ++i) {
+        float2 v;
+        split(i < H ? dw[i % H] : db[i % H], v.x, v.y);
+        __syncthreads();
+        red[wp][lane] = v;
+        __syncthreads();
+        if (wp == 0 && live) {
+            float2 s = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int v = 0; v < V; ++v) red[wp][lane * V + v] = q ? db[k][v] : dw[k][v];
-            __syncthreads();
-            for (int j = threadIdx.x; j < 32 * V; j += kTeamThreads) {
-                const int l = j / V, gj = col * (32 / lanes) + l / lanes, c = ((l & (lanes - 1)) + k * lanes) * V + j % V;
-                if (gj < a.G && c < a.P) {
-                    float s = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < W; ++i) s += red[i][j];
-                    part[((long long)split * 2 + q) * a.D + gj * a.P + c] = s;
-                }
-            }
+            for (int q = 0; q < W; ++q) s.x += red[q][lane].x, s.y += red[q][lane].y;
+            float *to = part + ((long long)split_ * 2 + i / H) * a.D + c0;
+            const int e = 2 * (i % H);                      // element of the thread, V a vector
+            const int ca = (t + e / V * lanes) * V + e % V, cb = (t + (e + 1) / V * lanes) * V + (e + 1) % V;
+            if (ca < a.P) to[ca] = s.x;
+            if (cb < a.P) to[cb] = s.y;
         }
+    }
+}
+
+// Sums of N values (1, 2 or 4) over a warp at once: afterwards the lanes of the
+// j-th N-th of the warp hold the sum of value j.
+template <int N>
+__device__ __forceinline__ float warp_sums(const float (&v)[N])
+{
+    const int lane = threadIdx.x & 31;
+    float s;
+    if constexpr (N == 1) {
+        s = v[0] + __shfl_xor_sync(0xffffffffu, v[0], 16);
+        s += __shfl_xor_sync(0xffffffffu, s, 8);
+    } else {
+        const bool hi = lane & 16;
+        float k[N / 2];
+#pragma unroll
+        for (int q = 0; q < N / 2; ++q)
+            k[q] = (hi ? v[N / 2 + q] : v[q]) + __shfl_xor_sync(0xffffffffu, hi ? v[q] : v[N / 2 + q], 16);
+        if constexpr (N == 2) {
+            s = k[0] + __shfl_xor_sync(0xffffffffu, k[0], 8);
+        } else {
+            const bool h8 = lane & 8;
+            s = (h8 ? k[1] : k[0]) + __shfl_xor_sync(0xffffffffu, h8 ? k[0] : k[1], 8);
+        }
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 4);
+    s += __shfl_xor_sync(0xffffffffu, s, 2);
+    s += __shfl_xor_sync(0xffffffffu, s, 1);
+    return s;
 }
 
 // A CTA keeps one group's columns and walks rows, R at a time: their sums meet
@@ -359,21 +506,21 @@ __global__ void __launch_bounds__(MAXT, 1)
 norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz, float *__restrict__ part)
 {
     extern __shared__ __align__(128) char ring[];
-    __shared__ float2 red[2][R][32];
+    __shared__ float red[2][2 * R][32];
     __shared__ uint64_t full[kMaxStages];
     __shared__ int abort_wait;
+    constexpr int H = V * NV / 2, N = 2 * R;
     constexpr bool KEEP = V * NV <= 8;
     const int t = threadIdx.x, n = blockDim.x, lane = t & 31, wp = t >> 5, nw = n >> 5;
-    const int g = blockIdx.x % a.G, split = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
+    const int g = blockIdx.x % a.G, split_ = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
     const float inv = 1.0f / a.P;
     const bool has_res = !GATE && a.dres != nullptr;
     const int row_t = a.P * (int)sizeof(T), row_g = has_res ? a.P * (int)sizeof(G) : 0;
     const int stage_bytes = (GATE ? 3 : 2) * row_t + row_g;
-    const int count = split < a.rows ? (int)((a.rows - split + nsplit - 1) / nsplit) : 0;     // rows of this CTA
-    const auto send = [&](int q) {                  // the CTA's q-th row
-        const int stage = q % nst;
+    const int count = split_ < a.rows ? (int)((a.rows - split_ + nsplit - 1) / nsplit) : 0;   // rows of this CTA
+    const auto send = [&](int q, int stage) {       // the CTA's q-th row
         char *to = ring + (size_t)stage * stage_bytes;
-        const long long row = split + (long long)q * nsplit, at = row * a.D + c0;
+        const long long row = split_ + (long long)q * nsplit, at = row * a.D + c0;
         tc::mbar_arrive_expect_tx(&full[stage], stage_bytes);
         tc::bulk_load(to, static_cast<const T *>(a.x) + row * a.xs + c0, row_t, &full[stage]);
         tc::bulk_load(to + row_t, static_cast<const T *>(a.dy) + at, row_t, &full[stage]);
@@ -384,22 +531,18 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
         abort_wait = 0;
         for (int k = 0; k < nst; ++k) tc::mbar_init(&full[k], 1);
         tc::mbar_fence_init();
-        for (int q = 0; q < min(nst, count); ++q) send(q);
+        for (int q = 0; q < min(nst, count); ++q) send(q, q);
     }
-    float dw[NV][V], db[NV][V], w[KEEP ? NV : 1][V];
+    F2 dw[H], db[H], w[H];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (t + k * n) * V;
-#pragma unroll
-        for (int v = 0; v < V; ++v) dw[k][v] = db[k][v] = w[KEEP ? k : 0][v] = 0.0f;
-        if (KEEP && c < a.P) load_values<float, V>(a.w + c0 + c, w[k]);
-    }
+    for (int i = 0; i < H; ++i) dw[i] = db[i] = f2(0.0f);
+    if (KEEP) load_params<V, NV>(a.w + c0, a.P, t, n, w);
     __syncthreads();
     float mu_next[R], rs_next[R];
     const auto stats = [&](int q, float &mu, float &rs) {
         mu = rs = 0.0f;
         if (q < count) {
-            const long long at = (split + (long long)q * nsplit) * a.G + g;
+            const long long at = (split_ + (long long)q * nsplit) * a.G + g;
             mu = a.mean[at], rs = a.rstd[at];
         }
     };
@@ -407,88 +550,50 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
     for (int r = 0; r < R; ++r) stats(r, mu_next[r], rs_next[r]);
     int stage = 0, parity = 0, turn = 0;
     for (int q = 0; q < count; q += R) {
-        float mu[R], rs[R];
-        Pack<T, V> xr[R][NV], zr[R][GATE ? NV : 1], dr[R][NV];
-        Raw<G, V> res[R][GATE ? 1 : NV];
+        BwdRow<T, G, V, NV, GATE> rows[R];
+        int used[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            mu[r] = mu_next[r], rs[r] = rs_next[r];
+            rows[r].mu = mu_next[r], rows[r].rs = rs_next[r];
             stats(q + R + r, mu_next[r], rs_next[r]);
             const bool there = q + r < count;
-            const long long row = split + (long long)(q + r) * nsplit, at = row * a.D + c0;
+            const long long row = split_ + (long long)(q + r) * nsplit, at = row * a.D + c0;
             const char *here = ring + (size_t)stage * stage_bytes;
             // a copy that does not arrive (2 s) is not waited for again: the row is then read in place
-            const bool staged = RING && there && tc::mbar_wait(&full[stage], parity, &abort_wait);
-            const T *x = staged ? reinterpret_cast<const T *>(here) : static_cast<const T *>(a.x) + row * a.xs + c0;
-            const T *dy = staged ? reinterpret_cast<const T *>(here + row_t) : static_cast<const T *>(a.dy) + at;
-            const T *z = !GATE ? nullptr : staged ? reinterpret_cast<const T *>(here + 2 * row_t)
-                                                  : static_cast<const T *>(a.z) + row * a.zs + c0;
-            const G *dres = !has_res ? nullptr : staged ? reinterpret_cast<const G *>(here + 2 * row_t)
-                                                        : static_cast<const G *>(a.dres) + at;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (t + k * n) * V;
-                if (there && c < a.P) {
-                    xr[r][k] = load_pack<T, V>(x + c);
-                    dr[r][k] = load_pack<T, V>(dy + c);
-                    if (GATE) zr[r][k] = load_pack<T, V>(z + c);
-                    if (!GATE && has_res) res[r][k].load(dres + c);
-                } else {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) xr[r][k].v[v] = dr[r][k].v[v] = zr[r][GATE ? k : 0].v[v] = from_f32<T>(0.0f);
-                }
-            }
+            if (RING && there && tc::mbar_wait(&full[stage], parity, &abort_wait))
+                rows[r].load(reinterpret_cast<const T *>(here), reinterpret_cast<const T *>(here + row_t),
+                             reinterpret_cast<const T *>(here + 2 * row_t),
+                             has_res ? reinterpret_cast<const G *>(here + 2 * row_t) : nullptr, a.P, t, n, true);
+            else
+                rows[r].load(static_cast<const T *>(a.x) + row * a.xs + c0, static_cast<const T *>(a.dy) + at,
+                             GATE ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr,
+                             has_res ? static_cast<const G *>(a.dres) + at : nullptr, a.P, t, n, there);
+            used[r] = stage;
             if (++stage == nst) stage = 0, parity ^= 1;
         }
+        if (!KEEP) load_params<V, NV>(a.w + c0, a.P, t, n, w);
+        float s[N];
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-            float s1 = 0.0f, s2 = 0.0f;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                Cols<V> cl;
-                const int c = (t + k * n) * V;
-                float wk[V];
-#pragma unroll
-                for (int v = 0; v < V; ++v) wk[v] = KEEP ? w[KEEP ? k : 0][v] : 0.0f;
-                if (!KEEP && c < a.P) load_values<float, V>(a.w + c0 + c, wk);
-                columns<T, V, GATE>(xr[r][k], zr[r][GATE ? k : 0], dr[r][k], wk, mu[r], rs[r], cl);
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    s1 += cl.wd[v];
-                    s2 = fmaf(cl.wd[v], cl.xh[v], s2);
-                    dw[k][v] = fmaf(cl.dy[v], cl.xh[v], dw[k][v]);
-                    db[k][v] += cl.dy[v];
-                }
-            }
-            s1 = team_sum(s1, 32);
-            s2 = team_sum(s2, 32);
-            if (lane == 0) red[turn][r][wp] = make_float2(s1, s2);
-        }
+        for (int r = 0; r < R; ++r) rows[r].sums(w, dw, db, s[2 * r], s[2 * r + 1]);
+        const float ws = warp_sums<N>(s);
+        if ((lane & (32 / N - 1)) == 0) red[turn][lane / (32 / N)][wp] = ws;
         __syncthreads();                            // the rows are in registers: their stages are free
         if (RING && t == 0)
+#pragma unroll
             for (int r = 0; r < R; ++r)
-                if (q + r + nst < count) send(q + r + nst);
+                if (q + r + nst < count) send(q + r + nst, used[r]);
+        // the warps' sums: the j-th N-th of each warp adds those of value j
+        float tot = 0.0f;
+        for (int k = lane & (32 / N - 1); k < nw; k += 32 / N) tot += red[turn][lane / (32 / N)][k];
+#pragma unroll
+        for (int o = 16 / N; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+        tot *= inv;
 #pragma unroll
         for (int r = 0; r < R; ++r) {
-            if (q + r >= count) break;
-            float2 s = make_float2(0.0f, 0.0f);
-            if (lane < nw) s = red[turn][r][lane];
-            const float s1 = team_sum(s.x, 32) * inv, s2 = team_sum(s.y, 32) * inv;
-            const long long at = (split + (long long)(q + r) * nsplit) * a.D + c0;
-#pragma unroll
-            for (int k = 0; k < NV; ++k) {
-                const int c = (t + k * n) * V;
-                if (c >= a.P) break;
-                Cols<V> cl;
-                float wk[V];
-                if (KEEP) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) wk[v] = w[KEEP ? k : 0][v];
-                } else {
-                    load_values<float, V>(a.w + c0 + c, wk);
-                }
-                columns<T, V, GATE>(xr[r][k], zr[r][GATE ? k : 0], dr[r][k], wk, mu[r], rs[r], cl);
-                write_columns<G, V, GATE>(cl, rs[r], s1, s2, has_res, res[r][GATE ? 0 : k], dx + at + c, GATE ? dz + at + c : nullptr);
+            const float s1 = __shfl_sync(0xffffffffu, tot, 2 * r * (32 / N)), s2 = __shfl_sync(0xffffffffu, tot, (2 * r + 1) * (32 / N));
+            if (q + r < count) {
+                const long long at = (split_ + (long long)(q + r) * nsplit) * a.D + c0;
+                rows[r].write(w, s1, s2, has_res, a.P, t, n, dx + at, GATE ? dz + at : nullptr);
             }
         }
         turn ^= 1;
@@ -497,8 +602,8 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
     for (int k = 0; k < NV; ++k) {
         const int c = (t + k * n) * V;
         if (c >= a.P) break;
-        store_values<float, V>(part + ((long long)split * 2) * a.D + c0 + c, dw[k]);
-        store_values<float, V>(part + ((long long)split * 2 + 1) * a.D + c0 + c, db[k]);
+        store_vector<float, V>(part + (long long)split_ * 2 * a.D + c0 + c, k, dw);
+        store_vector<float, V>(part + ((long long)split_ * 2 + 1) * a.D + c0 + c, k, db);
     }
 }
 
@@ -589,43 +694,49 @@ int lanes_of(int P, int V)
 // Whole warps that hold `vecs` vectors, nv a thread.
 int threads_of(int vecs, int nv) { return ((vecs + nv - 1) / nv + 31) / 32 * 32; }
 
+// CTAs of a team kernel: one for `per_sm` on every SM, as far as there are rows.
+int team_splits(int64_t rows, int ncols, int per_sm)
+{
+    const int64_t most = (rows + kTeamThreads / 32 - 1) / (kTeamThreads / 32);
+    return (int)std::min<int64_t>(most, std::max(1, sm_count() * per_sm / ncols));
+}
+
+int team_cols(int G, int lanes) { return (G + 32 / lanes - 1) / (32 / lanes); }
+
 template <typename T, int V, int NV, Mode M>
 void fwd_team(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStream_t st)
 {
-    const int lanes = lanes_of(a.P, V);
-    const unsigned per = kTeamThreads / lanes, units = (unsigned)(a.rows * a.G);
-    norm_fwd_team_kernel<T, V, NV, M><<<(units + per - 1) / per, kTeamThreads, 0, st>>>(a, lanes, y, sum, mean, rstd);
+    constexpr int R = V > 1 && NV == 1 ? 2 : 1;
+    const int lanes = lanes_of(a.P, V), ncols = team_cols(a.G, lanes), n = team_splits(a.rows, ncols, 8);
+    norm_fwd_team_kernel<T, V, NV, R, M><<<(unsigned)(ncols * n), kTeamThreads, 0, st>>>(a, lanes, ncols, y, sum, mean, rstd);
 }
 
-template <typename T, int V, int NV, Mode M>
+template <typename T, int V, int NV, Mode M, int MAXT>
 void fwd_cta(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStream_t st)
 {
-    norm_fwd_cta_kernel<T, V, NV, M>
+    norm_fwd_cta_kernel<T, V, NV, M, MAXT>
         <<<(unsigned)(a.rows * a.G), threads_of((a.P + V - 1) / V, NV), 0, st>>>(a, y, sum, mean, rstd);
 }
 
 // V elements a load (16 bytes or one).  A team holds up to 32 elements a lane,
-// a CTA's thread up to 16: 512 threads have 8192 elements, 1024 the longest group.
+// a CTA's thread 16: 512 threads have 8192 elements, 1024 the longest group.
 template <typename T, int V, Mode M>
 void fwd_mode(const NormArgs &a, void *y_, void *sum_, float *mean, float *rstd, cudaStream_t st)
 {
     T *y = static_cast<T *>(y_), *sum = static_cast<T *>(sum_);
-    const int vecs = (a.P + V - 1) / V;
     if constexpr (V == 1) {
-        if (a.P <= 32) fwd_team<T, 1, 1, M>(a, y, sum, mean, rstd, st);
-        else if (a.P <= 128) fwd_team<T, 1, 4, M>(a, y, sum, mean, rstd, st);
-        else if (a.P <= 512) fwd_team<T, 1, 16, M>(a, y, sum, mean, rstd, st);
-        else if (a.P <= 2048) fwd_cta<T, 1, 4, M>(a, y, sum, mean, rstd, st);
-        else fwd_cta<T, 1, 16, M>(a, y, sum, mean, rstd, st);
+        if (a.P <= 64) return fwd_team<T, 1, 2, M>(a, y, sum, mean, rstd, st);
+        if (a.P <= 256) return fwd_team<T, 1, 8, M>(a, y, sum, mean, rstd, st);
+        if (a.P <= 1024) return fwd_team<T, 1, 32, M>(a, y, sum, mean, rstd, st);
     } else {
-        constexpr int S = 16 / V;                   // vectors in 16 elements
-        if (vecs <= 32) fwd_team<T, V, 1, M>(a, y, sum, mean, rstd, st);
-        else if (vecs <= 64) fwd_team<T, V, 2, M>(a, y, sum, mean, rstd, st);
-        else if (vecs <= 128) fwd_team<T, V, 4, M>(a, y, sum, mean, rstd, st);
-        else if (vecs <= 384) fwd_cta<T, V, 1, M>(a, y, sum, mean, rstd, st);
-        else if (vecs <= 1024 || S == 2) fwd_cta<T, V, 2, M>(a, y, sum, mean, rstd, st);
-        else fwd_cta<T, V, S, M>(a, y, sum, mean, rstd, st);
+        const int vecs = (a.P + V - 1) / V;
+        if (vecs <= 32) return fwd_team<T, V, 1, M>(a, y, sum, mean, rstd, st);
+        if (vecs <= 64) return fwd_team<T, V, 2, M>(a, y, sum, mean, rstd, st);
+        if (vecs <= 128) return fwd_team<T, V, 4, M>(a, y, sum, mean, rstd, st);
     }
+    if (a.P <= 8 * 384) return fwd_cta<T, V, 8 / V, M, 384>(a, y, sum, mean, rstd, st);
+    if (a.P <= 8192) return fwd_cta<T, V, 16 / V, M, 512>(a, y, sum, mean, rstd, st);
+    return fwd_cta<T, V, 16 / V, M, 1024>(a, y, sum, mean, rstd, st);
 }
 
 template <typename T, int V>
@@ -663,9 +774,8 @@ Split split_of(const ssd_layer_norm_params &p, int V)
     const int64_t rows = std::max<int64_t>(p.rows, 1);
     if (s.team) {
         s.lanes = lanes_of(P, V);
-        s.ncols = (p.ngroups + 32 / s.lanes - 1) / (32 / s.lanes);
-        const int64_t most = (rows + kTeamThreads / 32 - 1) / (kTeamThreads / 32);
-        s.nsplit = (int)std::min<int64_t>(most, std::max(1, sm_count() * 4 / s.ncols));
+        s.ncols = team_cols(p.ngroups, s.lanes);
+        s.nsplit = team_splits(rows, s.ncols, 4);
     } else {
         s.per_sm = ctas_per_sm(P, V);
         s.ncols = p.ngroups;
@@ -682,7 +792,8 @@ struct BwdOut {
 template <typename T, typename G, int V, int NV, bool GATE>
 cudaError_t bwd_team(const NormArgs &a, const Split &s, const BwdOut &o, cudaStream_t st)
 {
-    norm_bwd_team_kernel<T, G, V, NV, GATE><<<(unsigned)(s.ncols * s.nsplit), kTeamThreads, 0, st>>>(
+    constexpr int R = V > 1 && NV == 1 && !GATE ? 2 : 1;
+    norm_bwd_team_kernel<T, G, V, NV, R, GATE><<<(unsigned)(s.ncols * s.nsplit), kTeamThreads, 0, st>>>(
         a, s.lanes, s.ncols, static_cast<G *>(o.dx), static_cast<G *>(o.dz), o.part);
     return cudaGetLastError();
 }
@@ -713,8 +824,7 @@ cudaError_t bwd_gate(const NormArgs &a, const Split &s, const BwdOut &o, cudaStr
     const int vecs = (a.P + V - 1) / V;
     if constexpr (V == 1) {
         if (s.team) {
-            if (a.P <= 32) return bwd_team<T, G, 1, 1, GATE>(a, s, o, st);
-            return a.P <= 128 ? bwd_team<T, G, 1, 4, GATE>(a, s, o, st) : bwd_team<T, G, 1, 8, GATE>(a, s, o, st);
+            return a.P <= 64 ? bwd_team<T, G, 1, 2, GATE>(a, s, o, st) : bwd_team<T, G, 1, 8, GATE>(a, s, o, st);
         }
     } else {
         if (s.team) {

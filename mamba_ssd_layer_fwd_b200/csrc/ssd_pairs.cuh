@@ -1,0 +1,77 @@
+// Paired float32 arithmetic and the hardware approximations.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace ssd {
+
+__device__ __forceinline__ float ex2_approx(float v)
+{
+    float o;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+__device__ __forceinline__ float rcp_approx(float v)
+{
+    float o;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+__device__ __forceinline__ float rsqrt_approx(float v)
+{
+    float o;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(v));
+    return o;
+}
+
+// Two float32 in a register pair: sm_100's paired instructions do two
+// operations for one issue slot, and issue slots are what the elementwise
+// kernels run out of next after HBM.
+struct F2 {
+    unsigned long long v;
+};
+__device__ __forceinline__ F2 f2(float x, float y)
+{
+    F2 o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o.v) : "f"(x), "f"(y));
+    return o;
+}
+__device__ __forceinline__ F2 f2(float x) { return f2(x, x); }
+__device__ __forceinline__ void split(F2 a, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(a.v)); }
+__device__ __forceinline__ F2 mul(F2 a, F2 b)
+{
+    F2 o;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+    return o;
+}
+__device__ __forceinline__ F2 add(F2 a, F2 b)
+{
+    F2 o;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o.v) : "l"(a.v), "l"(b.v));
+    return o;
+}
+__device__ __forceinline__ F2 fma(F2 a, F2 b, F2 c)
+{
+    F2 o;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return o;
+}
+template <typename Op>
+__device__ __forceinline__ F2 each(F2 a, Op op)
+{
+    float x, y;
+    split(a, x, y);
+    return f2(op(x), op(y));
+}
+__device__ __forceinline__ F2 shown(float2 a) { return f2(a.x, a.y); }
+
+__device__ __forceinline__ uint32_t pack_bf16(F2 a)
+{
+    float x, y;
+    split(a, x, y);
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+}  // namespace ssd
