@@ -141,14 +141,24 @@ template <typename T, int V, int NV, Mode M> struct FwdRow {
 
     __device__ __forceinline__ void load(const NormArgs &a, long long row, int c0, int t, int n, bool live)
     {
-        const T *xp = static_cast<const T *>(a.x) + row * a.xs + c0;
-        const T *zp = M == kGate       ? static_cast<const T *>(a.z) + row * a.zs + c0
-                      : M == kResidual ? static_cast<const T *>(a.res) + row * a.D + c0
-                                       : nullptr;
+        load(x_of(a, row, c0), z_of(a, row, c0), a.P, t, n, live);
+    }
+    static __device__ __forceinline__ const T *x_of(const NormArgs &a, long long row, int c0)
+    {
+        return static_cast<const T *>(a.x) + row * a.xs + c0;
+    }
+    // the second input: z or the residual
+    static __device__ __forceinline__ const T *z_of(const NormArgs &a, long long row, int c0)
+    {
+        if (M == kGate) return static_cast<const T *>(a.z) + row * a.zs + c0;
+        return M == kResidual ? static_cast<const T *>(a.res) + row * a.D + c0 : nullptr;
+    }
+    __device__ __forceinline__ void load(const T *xp, const T *zp, int P, int t, int n, bool live)
+    {
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
             const int c = (t + k * n) * V;
-            if (live && c < a.P) {
+            if (live && c < P) {
                 x.load(k, xp + c);
                 if (M != kPlain) z.load(k, zp + c);
             } else {
@@ -305,12 +315,68 @@ norm_fwd_cta_kernel(NormArgs a, T *__restrict__ y, T *__restrict__ sum, float *_
     const float inv = 1.0f / a.P;
     FwdRow<T, V, NV, M> r;
     r.load(a, row, c0, t, n, true);
-    F2 w[H], b[H];
-    load_params<V, NV>(a.w + c0, a.P, t, n, w);
-    load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
     const float mu = mean_of(cta_sum(r.input(a, row, c0, t, n, true, sum), slots[0]), a.P, inv);
     const float rs = rsqrtf(fmaf(cta_sum(r.centre(a, mu, t, n), slots[1]), inv, a.eps));
+    F2 w[H], b[H];                                  // from L1 by now; registers make room for more CTAs
+    load_params<V, NV>(a.w + c0, a.P, t, n, w);
+    load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
     r.write(a, row, g, t, n, true, mu, rs, w, b, y, mean, rstd);
+}
+
+// The same for many rows that are aligned to 16 bytes: a CTA keeps one group's
+// columns and walks rows that thread 0 copies `nst` ahead into shared memory,
+// so that HBM reads go on through the two reductions of a row.
+constexpr int kMaxStages = 6;
+
+template <typename T, int V, int NV, Mode M>
+__global__ void __launch_bounds__(384, 2)
+norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean,
+                     float *__restrict__ rstd)
+{
+    extern __shared__ __align__(128) char ring[];
+    __shared__ float slots[2][32];
+    __shared__ uint64_t full[kMaxStages];
+    __shared__ int abort_wait;
+    constexpr int H = V * NV / 2;
+    const int t = threadIdx.x, n = blockDim.x;
+    const int g = blockIdx.x % a.G, split_ = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
+    const float inv = 1.0f / a.P;
+    const int bytes = a.P * (int)sizeof(T), stage_bytes = M == kPlain ? bytes : 2 * bytes;
+    const int count = split_ < a.rows ? (int)((a.rows - split_ + nsplit - 1) / nsplit) : 0;   // rows of this CTA
+    typedef FwdRow<T, V, NV, M> Row;
+    const auto send = [&](int q, int stage) {       // the CTA's q-th row
+        char *to = ring + (size_t)stage * stage_bytes;
+        const long long row = split_ + (long long)q * nsplit;
+        tc::mbar_arrive_expect_tx(&full[stage], stage_bytes);
+        tc::bulk_load(to, Row::x_of(a, row, c0), bytes, &full[stage]);
+        if (M != kPlain) tc::bulk_load(to + bytes, Row::z_of(a, row, c0), bytes, &full[stage]);
+    };
+    if (t == 0) {
+        abort_wait = 0;
+        for (int k = 0; k < nst; ++k) tc::mbar_init(&full[k], 1);
+        tc::mbar_fence_init();
+        for (int q = 0; q < min(nst, count); ++q) send(q, q);
+    }
+    __syncthreads();
+    int stage = 0, parity = 0;
+    for (int q = 0; q < count; ++q) {
+        const long long row = split_ + (long long)q * nsplit;
+        const char *here = ring + (size_t)stage * stage_bytes;
+        Row r;
+        // a copy that does not arrive (2 s) is not waited for again: the row is then read in place
+        if (tc::mbar_wait(&full[stage], parity, &abort_wait))
+            r.load(reinterpret_cast<const T *>(here), reinterpret_cast<const T *>(here + bytes), a.P, t, n, true);
+        else
+            r.load(a, row, c0, t, n, true);
+        const float mu = mean_of(cta_sum(r.input(a, row, c0, t, n, true, sum), slots[0]), a.P, inv);
+        if (t == 0 && q + nst < count) send(q + nst, stage);    // a barrier ago the row was in registers
+        const float rs = rsqrtf(fmaf(cta_sum(r.centre(a, mu, t, n), slots[1]), inv, a.eps));
+        F2 w[H], b[H];
+        load_params<V, NV>(a.w + c0, a.P, t, n, w);
+        load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
+        r.write(a, row, g, t, n, true, mu, rs, w, b, y, mean, rstd);
+        if (++stage == nst) stage = 0, parity ^= 1;
+    }
 }
 
 // ---------------------------------------------------------------- backward
@@ -499,7 +565,6 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N])
 // otherwise threads load their own columns.  The weights stay in registers
 // where a thread has eight elements, and are read again for each row, from L1,
 // where it has sixteen.
-constexpr int kMaxStages = 6;
 
 template <typename T, typename G, int V, int NV, int R, bool GATE, bool RING, int MAXT>
 __global__ void __launch_bounds__(MAXT, 1)
@@ -718,6 +783,21 @@ void fwd_cta(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStre
         <<<(unsigned)(a.rows * a.G), threads_of((a.P + V - 1) / V, NV), 0, st>>>(a, y, sum, mean, rstd);
 }
 
+template <typename T, int V, int NV, Mode M>
+bool fwd_ring(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStream_t st)
+{
+    const int t = threads_of((a.P + V - 1) / V, NV), per_sm = std::min(6, 65536 / (80 * t));
+    const int n = sm_count() * per_sm / a.G;
+    if (n < 1 || a.rows < 2 * n) return false;      // a row or two a CTA: nothing to copy ahead
+    const auto kernel = norm_fwd_ring_kernel<T, V, NV, M>;
+    const size_t stage = (size_t)a.P * sizeof(T) * (M == kPlain ? 1 : 2);
+    const int nst = (int)std::min<size_t>(kMaxStages, (size_t)216 * 1024 / per_sm / stage);
+    if (nst < 2 || cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)(nst * stage)) != cudaSuccess)
+        return false;
+    kernel<<<(unsigned)(a.G * n), t, nst * stage, st>>>(a, nst, y, sum, mean, rstd);
+    return true;
+}
+
 // V elements a load (16 bytes or one).  A team holds up to 32 elements a lane,
 // a CTA's thread 16: 512 threads have 8192 elements, 1024 the longest group.
 template <typename T, int V, Mode M>
@@ -733,6 +813,10 @@ void fwd_mode(const NormArgs &a, void *y_, void *sum_, float *mean, float *rstd,
         if (vecs <= 32) return fwd_team<T, V, 1, M>(a, y, sum, mean, rstd, st);
         if (vecs <= 64) return fwd_team<T, V, 2, M>(a, y, sum, mean, rstd, st);
         if (vecs <= 128) return fwd_team<T, V, 4, M>(a, y, sum, mean, rstd, st);
+    }
+    if constexpr (V > 1) {
+        if (a.P <= 8 * 256 && fwd_ring<T, V, 8 / V, M>(a, y, sum, mean, rstd, st)) return;
+        if (a.P > 8 * 256 && a.P <= 16 * 384 && fwd_ring<T, V, 16 / V, M>(a, y, sum, mean, rstd, st)) return;
     }
     if (a.P <= 8 * 384) return fwd_cta<T, V, 8 / V, M, 384>(a, y, sum, mean, rstd, st);
     if (a.P <= 8192) return fwd_cta<T, V, 16 / V, M, 512>(a, y, sum, mean, rstd, st);
