@@ -15,6 +15,7 @@
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>
+#include <type_traits>
 
 #include "ssd_common.cuh"
 #include "ssd_norm.h"
@@ -384,6 +385,7 @@ norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum
 // A thread's part of one row.
 template <typename T, typename G, int V, int NV, bool GATE> struct BwdRow {
     static constexpr int H = V * NV / 2;
+    static constexpr int NP = V == 1 ? 1 : NV, HP = H / NP;     // pieces (vectors) and their pairs
     Raw<T, V, NV> x, dy;
     Raw<T, V, GATE ? NV : 2> z;
     RawGrad<G, V, GATE ? 2 : NV> dres;
@@ -419,48 +421,91 @@ template <typename T, typename G, int V, int NV, bool GATE> struct BwdRow {
     }
 
     // sums of w dy and w dy xhat over the thread's elements; dw and db go on
-    __device__ __forceinline__ void sums(const F2 (&w)[H], F2 (&dw)[H], F2 (&db)[H], float &s1, float &s2) const
+    template <typename W>
+    __device__ __forceinline__ void sums(const W &weights, F2 (&dw)[H], F2 (&db)[H], float &s1, float &s2) const
     {
         F2 a = f2(0.0f), b = f2(0.0f);
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            const F2 d = dy.pair(i), wd = mul(d, w[i]), xh = hat(i);
-            a = add(a, wd);
-            b = fma(wd, xh, b);
-            dw[i] = fma(d, xh, dw[i]);
-            db[i] = add(db[i], d);
+        for (int k = 0; k < NP; ++k) {
+            F2 w[HP];
+            weights(k, w);
+#pragma unroll
+            for (int j = 0; j < HP; ++j) {
+                const int i = k * HP + j;
+                const F2 d = dy.pair(i), wd = mul(d, w[j]), xh = hat(i);
+                a = add(a, wd);
+                b = fma(wd, xh, b);
+                dw[i] = fma(d, xh, dw[i]);
+                db[i] = add(db[i], d);
+            }
         }
         s1 = total(a), s2 = total(b);
     }
 
-    __device__ __forceinline__ void write(const F2 (&w)[H], float s1, float s2, bool has_res, int P, int t, int n, G *dx,
+    template <typename W>
+    __device__ __forceinline__ void write(const W &weights, float s1, float s2, bool has_res, int P, int t, int n, G *dx,
                                           G *dz) const
     {
         F2 o[H], oz[GATE ? H : 1];
 #pragma unroll
-        for (int i = 0; i < H; ++i) {
-            F2 xv = x.pair(i), zv, sz, u = xv;
-            if constexpr (GATE) {
-                zv = z.pair(i), sz = sigmoid2(zv);
-                u = mul(xv, mul(zv, sz));
-            }
-            const F2 xh = mul(add(u, negated(mu)), f2(rs));
-            const F2 du = mul(fma(xh, f2(-s2), fma(dy.pair(i), w[i], f2(-s1))), f2(rs));
-            if constexpr (GATE) {
-                o[i] = mul(du, mul(zv, sz));
-                // silu' = s (1 + z (1 - s))
-                oz[i] = mul(mul(du, xv), mul(sz, fma(zv, fma(sz, f2(-1.0f), f2(1.0f)), f2(1.0f))));
-            } else {
-                o[i] = has_res ? add(du, dres.pair(i)) : du;
-            }
-        }
+        for (int k = 0; k < NP; ++k) {
+            F2 w[HP];
+            weights(k, w);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (t + k * n) * V;
-            if (c >= P) break;
-            store_vector<G, V>(dx + c, k, o);
-            if constexpr (GATE) store_vector<G, V>(dz + c, k, oz);
+            for (int j = 0; j < HP; ++j) {
+                const int i = k * HP + j;
+                F2 xv = x.pair(i), zv, sz, u = xv;
+                if constexpr (GATE) {
+                    zv = z.pair(i), sz = sigmoid2(zv);
+                    u = mul(xv, mul(zv, sz));
+                }
+                const F2 xh = mul(add(u, negated(mu)), f2(rs));
+                const F2 du = mul(fma(xh, f2(-s2), fma(dy.pair(i), w[j], f2(-s1))), f2(rs));
+                if constexpr (GATE) {
+                    o[i] = mul(du, mul(zv, sz));
+                    // silu' = s (1 + z (1 - s))
+                    oz[i] = mul(mul(du, xv), mul(sz, fma(zv, fma(sz, f2(-1.0f), f2(1.0f)), f2(1.0f))));
+                } else {
+                    o[i] = has_res ? add(du, dres.pair(i)) : du;
+                }
+            }
+            if constexpr (V > 1) {
+                const int c = (t + k * n) * V;
+                if (c < P) {
+                    store_vector<G, V>(dx + c, k, o);
+                    if constexpr (GATE) store_vector<G, V>(dz + c, k, oz);
+                }
+            }
         }
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                const int c = t + k * n;
+                if (c >= P) break;
+                store_vector<G, V>(dx + c, k, o);
+                if constexpr (GATE) store_vector<G, V>(dz + c, k, oz);
+            }
+        }
+    }
+};
+
+// Weights of the k-th piece of a thread's columns: kept in registers, or read
+// where they are used.
+template <int H, int HP> struct KeptWeights {
+    const F2 (&all)[H];
+    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
+    {
+#pragma unroll
+        for (int j = 0; j < HP; ++j) w[j] = all[k * HP + j];
+    }
+};
+template <int V, int NV, int HP> struct ReadWeights {
+    const float *p;
+    int P, t, n;
+    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
+    {
+        if constexpr (V == 1) load_params<1, NV>(p, P, t, n, w);
+        else load_params<V, 1>(p, P, t + k * n, n, w);
     }
 };
 
@@ -478,12 +523,14 @@ norm_bwd_team_kernel(NormArgs a, int lanes, int ncols, G *__restrict__ dx, G *__
     const int g = col * (32 / lanes) + lane / lanes, c0 = g * a.P;
     const bool live = g < a.G;
     const float inv = 1.0f / a.P;
-    F2 w[H], dw[H], db[H];
-    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, w);
+    typedef BwdRow<T, G, V, NV, GATE> Row;
+    F2 wk[H], dw[H], db[H];
+    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, wk);
+    const KeptWeights<H, Row::HP> w{wk};
 #pragma unroll
     for (int i = 0; i < H; ++i) dw[i] = db[i] = f2(0.0f);
     for (long long row0 = (long long)split_ * W + wp; row0 < a.rows; row0 += R * step) {
-        BwdRow<T, G, V, NV, GATE> r[R];
+        Row r[R];
         float s1[R], s2[R];
 #pragma unroll
         for (int k = 0; k < R; ++k) {
@@ -566,8 +613,8 @@ __device__ __forceinline__ float warp_sums(const float (&v)[N])
 // where a thread has eight elements, and are read again for each row, from L1,
 // where it has sixteen.
 
-template <typename T, typename G, int V, int NV, int R, bool GATE, bool RING, int MAXT>
-__global__ void __launch_bounds__(MAXT, 1)
+template <typename T, typename G, int V, int NV, int R, bool GATE, bool RING, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB)
 norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz, float *__restrict__ part)
 {
     extern __shared__ __align__(128) char ring[];
@@ -575,7 +622,7 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
     __shared__ uint64_t full[kMaxStages];
     __shared__ int abort_wait;
     constexpr int H = V * NV / 2, N = 2 * R;
-    constexpr bool KEEP = V * NV <= 8;
+    constexpr bool KEEP = V * NV <= 8 && MINB == 1;
     const int t = threadIdx.x, n = blockDim.x, lane = t & 31, wp = t >> 5, nw = n >> 5;
     const int g = blockIdx.x % a.G, split_ = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
     const float inv = 1.0f / a.P;
@@ -598,10 +645,16 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
         tc::mbar_fence_init();
         for (int q = 0; q < min(nst, count); ++q) send(q, q);
     }
-    F2 dw[H], db[H], w[H];
+    typedef BwdRow<T, G, V, NV, GATE> Row;
+    F2 dw[H], db[H], wk[H];
 #pragma unroll
     for (int i = 0; i < H; ++i) dw[i] = db[i] = f2(0.0f);
-    if (KEEP) load_params<V, NV>(a.w + c0, a.P, t, n, w);
+    if (KEEP) load_params<V, NV>(a.w + c0, a.P, t, n, wk);
+    typedef std::conditional_t<KEEP, KeptWeights<H, Row::HP>, ReadWeights<V, NV, Row::HP>> Weights;
+    const Weights w = [&] {
+        if constexpr (KEEP) return Weights{wk};
+        else return Weights{a.w + c0, a.P, t, n};
+    }();
     __syncthreads();
     float mu_next[R], rs_next[R];
     const auto stats = [&](int q, float &mu, float &rs) {
@@ -615,7 +668,7 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
     for (int r = 0; r < R; ++r) stats(r, mu_next[r], rs_next[r]);
     int stage = 0, parity = 0, turn = 0;
     for (int q = 0; q < count; q += R) {
-        BwdRow<T, G, V, NV, GATE> rows[R];
+        Row rows[R];
         int used[R];
 #pragma unroll
         for (int r = 0; r < R; ++r) {
@@ -636,7 +689,6 @@ norm_bwd_cta_kernel(NormArgs a, int nst, G *__restrict__ dx, G *__restrict__ dz,
             used[r] = stage;
             if (++stage == nst) stage = 0, parity ^= 1;
         }
-        if (!KEEP) load_params<V, NV>(a.w + c0, a.P, t, n, w);
         float s[N];
 #pragma unroll
         for (int r = 0; r < R; ++r) rows[r].sums(w, dw, db, s[2 * r], s[2 * r + 1]);
@@ -847,7 +899,7 @@ struct Split {
 int ctas_per_sm(int P, int V)
 {
     const int vecs = (P + V - 1) / V, nv = vectors_of(vecs, V);
-    return nv * V == 8 ? std::max(1, std::min(8, 65536 / (80 * threads_of(vecs, nv)))) : 1;
+    return nv * V == 8 ? (V > 1 && P > 8 * 320 && P <= 16 * 320 ? 2 : std::max(1, std::min(8, 65536 / (80 * threads_of(vecs, nv))))) : 1;
 }
 
 Split split_of(const ssd_layer_norm_params &p, int V)
@@ -882,11 +934,11 @@ cudaError_t bwd_team(const NormArgs &a, const Split &s, const BwdOut &o, cudaStr
     return cudaGetLastError();
 }
 
-template <typename T, typename G, int V, int NV, int R, bool GATE, int MAXT>
+template <typename T, typename G, int V, int NV, int R, bool GATE, int MAXT, int MINB = 1>
 cudaError_t bwd_cta(const NormArgs &a, const Split &s, const BwdOut &o, cudaStream_t st)
 {
     constexpr bool RING = V > 1;
-    const auto kernel = norm_bwd_cta_kernel<T, G, V, NV, R, GATE, RING, MAXT>;
+    const auto kernel = norm_bwd_cta_kernel<T, G, V, NV, R, GATE, RING, MAXT, MINB>;
     size_t smem = 0;
     int nst = 1;
     if (RING) {
@@ -917,6 +969,8 @@ cudaError_t bwd_gate(const NormArgs &a, const Split &s, const BwdOut &o, cudaStr
             if constexpr (V == 4) return bwd_team<T, G, V, 4, GATE>(a, s, o, st);
         }
     }
+    if constexpr (V > 1 && !GATE)
+        if (s.per_sm >= 2 && vecs * V > 8 * 320 && vecs * V <= 16 * 320) return bwd_cta<T, G, V, 16 / V, 1, GATE, 320, 2>(a, s, o, st);
     if (vectors_of(vecs, V) * V == 8) return bwd_cta<T, G, V, 8 / V, GATE ? 1 : 2, GATE, kCtaThreads>(a, s, o, st);
     if (vecs * V <= 8192) return bwd_cta<T, G, V, 16 / V, 1, GATE, 512>(a, s, o, st);
     return bwd_cta<T, G, V, 16 / V, 1, GATE, 1024>(a, s, o, st);
