@@ -214,22 +214,6 @@ __device__ __forceinline__ void store4(T *p, const F4 &f, int n)
     }
 }
 
-// ---------------------------------------------------------------- copies global -> shared
-// BYTES = 16, 8 or 4 (both addresses aligned to it); `in` false: zeros.
-template <int BYTES>
-__device__ __forceinline__ void copy_async(void *to, const void *from, bool in)
-{
-    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
-    const int n = in ? BYTES : 0;
-    if constexpr (BYTES == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
-    else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(from), "r"(n), "n"(BYTES) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
 // ---------------------------------------------------------------- vectors of V adjacent channels
 template <typename T, int V>
 struct alignas(sizeof(T) * V) Vec {

@@ -268,12 +268,27 @@ __device__ __forceinline__ void load_params(const float *p, int P, int t, int n,
     for (int i = 0; i < V * NV / 2; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
-constexpr int kTeamThreads = 256;
+// A lane's own ring in shared memory for kDepth rows of N pieces of 16 bytes and
+// two floats: it copies its vectors kDepth - 1 rows ahead and reads them back
+// itself, so nothing but its own copies is waited for.
+constexpr int kDepth = 4;
+template <int N> struct LaneRing {
+    static constexpr int kRow = N * 512 + 256, kWarp = kDepth * kRow;
+    char *base;
+    __device__ __forceinline__ LaneRing(char *smem, int warp, int lane) : base(smem + warp * kWarp + lane * 16) {}
+    __device__ __forceinline__ char *piece(int stage, int k) const { return base + stage * kRow + k * 512; }
+    __device__ __forceinline__ float *number(int stage, int k, int lane) const
+    {
+        return reinterpret_cast<float *>(base - lane * 16 + stage * kRow + N * 512 + k * 128) + lane;
+    }
+};
+
+constexpr int kTeamThreads = 256, kFwdTeamCtas = 5, kBwdTeamCtas = 2;     // CTAs an SM
 
 // A warp has 32 / lanes neighbouring groups of a row (lanes: 8, 16 or 32 with
 // lanes V NV >= P) and walks rows, R at a time.
 template <typename T, int V, int NV, int R, Mode M>
-__global__ void __launch_bounds__(kTeamThreads, 2)
+__global__ void __launch_bounds__(kTeamThreads, V * NV <= 8 ? kFwdTeamCtas : 2)
 norm_fwd_team_kernel(NormArgs a, int lanes, int ncols, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean,
                      float *__restrict__ rstd)
 {
@@ -509,13 +524,14 @@ template <int V, int NV, int HP> struct ReadWeights {
     }
 };
 
-// Warps of a CTA share 32 / lanes neighbouring groups and take rows in turn, R
-// at a time.  part: [CTA of the columns][2][D].
-template <typename T, typename G, int V, int NV, int R, bool GATE>
-__global__ void __launch_bounds__(kTeamThreads, 2)
+// Warps of a CTA share 32 / lanes neighbouring groups and take rows in turn.
+// part: [CTA of the columns][2][D].
+template <typename T, typename G, int V, int NV, bool GATE>
+__global__ void __launch_bounds__(kTeamThreads, V * NV <= 8 ? kBwdTeamCtas : 2)
 norm_bwd_team_kernel(NormArgs a, int lanes, int ncols, G *__restrict__ dx, G *__restrict__ dz, float *__restrict__ part)
 {
     constexpr int W = kTeamThreads / 32, H = V * NV / 2;
+    extern __shared__ __align__(128) char ring[];
     __shared__ float2 red[W][32];
     const int lane = threadIdx.x & 31, wp = threadIdx.x >> 5, t = lane & (lanes - 1);
     const int col = blockIdx.x % ncols, split_ = blockIdx.x / ncols;
@@ -529,31 +545,81 @@ norm_bwd_team_kernel(NormArgs a, int lanes, int ncols, G *__restrict__ dx, G *__
     const KeptWeights<H, Row::HP> w{wk};
 #pragma unroll
     for (int i = 0; i < H; ++i) dw[i] = db[i] = f2(0.0f);
-    for (long long row0 = (long long)split_ * W + wp; row0 < a.rows; row0 += R * step) {
-        Row r[R];
-        float s1[R], s2[R];
+    const long long first = (long long)split_ * W + wp;
+    const auto process = [&](const Row &r, long long row) {
+        float s1, s2;
+        r.sums(w, dw, db, s1, s2);
+        s1 = team_sum(s1, lanes) * inv;
+        s2 = team_sum(s2, lanes) * inv;
+        const long long at = row * a.D + c0;
+        if (live) r.write(w, s1, s2, !GATE && a.dres, a.P, t, lanes, dx + at, GATE ? dz + at : nullptr);
+    };
+    if constexpr (V > 1 && V * NV <= 8) {
+        constexpr int NR = V * (int)sizeof(G) / 16;     // pieces of a vector of dresidual
+        const LaneRing<NV * (GATE ? 3 : 2 + NR)> lr(ring, wp, lane);
+        const auto copy = [&](long long row, int stage) {
+            const long long at = row * a.D + c0;
+            if (live && row < a.rows) {
 #pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const long long row = row0 + k * step, at = row * a.D + c0;
-            const bool there = live && row < a.rows;
-            r[k].mu = r[k].rs = 0.0f;
-            if (there) r[k].mu = a.mean[row * a.G + g], r[k].rs = a.rstd[row * a.G + g];
-            r[k].load(static_cast<const T *>(a.x) + row * a.xs + c0, static_cast<const T *>(a.dy) + at,
-                      GATE ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr,
-                      !GATE && a.dres ? static_cast<const G *>(a.dres) + at : nullptr, a.P, t, lanes, there);
+                for (int k = 0; k < NV; ++k) {
+                    const int c = (t + k * lanes) * V;
+                    if (c >= a.P) break;
+                    copy_async<16>(lr.piece(stage, k), static_cast<const T *>(a.x) + row * a.xs + c0 + c, true);
+                    copy_async<16>(lr.piece(stage, NV + k), static_cast<const T *>(a.dy) + at + c, true);
+                    if constexpr (GATE) {
+                        copy_async<16>(lr.piece(stage, 2 * NV + k), static_cast<const T *>(a.z) + row * a.zs + c0 + c, true);
+                    } else if (a.dres) {
+#pragma unroll
+                        for (int q = 0; q < NR; ++q)
+                            copy_async<16>(lr.piece(stage, 2 * NV + k * NR + q),
+                                           static_cast<const G *>(a.dres) + at + c + q * (16 / (int)sizeof(G)), true);
+                    }
+                }
+                copy_async<4>(lr.number(stage, 0, lane), a.mean + row * a.G + g, true);
+                copy_async<4>(lr.number(stage, 1, lane), a.rstd + row * a.G + g, true);
+            }
+            copy_commit();
+        };
+        for (int k = 0; k < kDepth - 1; ++k) copy(first + k * step, k);
+        int stage = 0;
+        for (long long row = first; row < a.rows; row += step) {
+            copy(row + (kDepth - 1) * step, (stage + kDepth - 1) % kDepth);
+            copy_wait<kDepth - 1>();
+            Row r;
+            r.mu = live ? *lr.number(stage, 0, lane) : 0.0f;
+            r.rs = live ? *lr.number(stage, 1, lane) : 0.0f;
+#pragma unroll
+            for (int k = 0; k < NV; ++k) {
+                if (live && (t + k * lanes) * V < a.P) {
+                    r.x.load(k, reinterpret_cast<const T *>(lr.piece(stage, k)));
+                    r.dy.load(k, reinterpret_cast<const T *>(lr.piece(stage, NV + k)));
+                    if constexpr (GATE) {
+                        r.z.load(k, reinterpret_cast<const T *>(lr.piece(stage, 2 * NV + k)));
+                    } else if (a.dres) {
+#pragma unroll
+                        for (int q = 0; q < NR; ++q)
+                            r.dres.r.load(k * NR + q, reinterpret_cast<const G *>(lr.piece(stage, 2 * NV + k * NR + q)));
+                    }
+                } else {
+                    r.x.zero(k);
+                    r.dy.zero(k);
+                    if constexpr (GATE) r.z.zero(k);
+                }
+            }
+            process(r, row);
+            stage = (stage + 1) % kDepth;
         }
-#pragma unroll
-        for (int k = 0; k < R; ++k) r[k].sums(w, dw, db, s1[k], s2[k]);
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            s1[k] = team_sum(s1[k], lanes) * inv;
-            s2[k] = team_sum(s2[k], lanes) * inv;
-        }
-#pragma unroll
-        for (int k = 0; k < R; ++k) {
-            const long long row = row0 + k * step, at = row * a.D + c0;
-            if (live && row < a.rows)
-                r[k].write(w, s1[k], s2[k], !GATE && a.dres, a.P, t, lanes, dx + at, GATE ? dz + at : nullptr);
+        copy_wait<0>();
+    } else {
+        for (long long row = first; row < a.rows; row += step) {
+            const long long at = row * a.D + c0;
+            Row r;
+            r.mu = r.rs = 0.0f;
+            if (live) r.mu = a.mean[row * a.G + g], r.rs = a.rstd[row * a.G + g];
+            r.load(static_cast<const T *>(a.x) + row * a.xs + c0, static_cast<const T *>(a.dy) + at,
+                   GATE ? static_cast<const T *>(a.z) + row * a.zs + c0 : nullptr,
+                   !GATE && a.dres ? static_cast<const G *>(a.dres) + at : nullptr, a.P, t, lanes, live);
+            process(r, row);
         }
     }
     // the warps' sums, in order
@@ -823,8 +889,8 @@ int team_cols(int G, int lanes) { return (G + 32 / lanes - 1) / (32 / lanes); }
 template <typename T, int V, int NV, Mode M>
 void fwd_team(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStream_t st)
 {
-    constexpr int R = V > 1 && NV == 1 ? 2 : 1;
-    const int lanes = lanes_of(a.P, V), ncols = team_cols(a.G, lanes), n = team_splits(a.rows, ncols, 8);
+    constexpr int R = 1;
+    const int lanes = lanes_of(a.P, V), ncols = team_cols(a.G, lanes), n = team_splits(a.rows, ncols, V * NV <= 8 ? kFwdTeamCtas : 2);
     norm_fwd_team_kernel<T, V, NV, R, M><<<(unsigned)(ncols * n), kTeamThreads, 0, st>>>(a, lanes, ncols, y, sum, mean, rstd);
 }
 
@@ -911,7 +977,7 @@ Split split_of(const ssd_layer_norm_params &p, int V)
     if (s.team) {
         s.lanes = lanes_of(P, V);
         s.ncols = team_cols(p.ngroups, s.lanes);
-        s.nsplit = team_splits(rows, s.ncols, 4);
+        s.nsplit = team_splits(rows, s.ncols, kBwdTeamCtas);
     } else {
         s.per_sm = ctas_per_sm(P, V);
         s.ncols = p.ngroups;
@@ -928,9 +994,15 @@ struct BwdOut {
 template <typename T, typename G, int V, int NV, bool GATE>
 cudaError_t bwd_team(const NormArgs &a, const Split &s, const BwdOut &o, cudaStream_t st)
 {
-    constexpr int R = V > 1 && NV == 1 && !GATE ? 2 : 1;
-    norm_bwd_team_kernel<T, G, V, NV, R, GATE><<<(unsigned)(s.ncols * s.nsplit), kTeamThreads, 0, st>>>(
-        a, s.lanes, s.ncols, static_cast<G *>(o.dx), static_cast<G *>(o.dz), o.part);
+    const auto kernel = norm_bwd_team_kernel<T, G, V, NV, GATE>;
+    int smem = 0;
+    if constexpr (V > 1 && V * NV <= 8) {
+        smem = kTeamThreads / 32 * LaneRing<NV * (GATE ? 3 : 2 + V * (int)sizeof(G) / 16)>::kWarp;
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+    }
+    kernel<<<(unsigned)(s.ncols * s.nsplit), kTeamThreads, smem, st>>>(a, s.lanes, s.ncols, static_cast<G *>(o.dx),
+                                                                       static_cast<G *>(o.dz), o.part);
     return cudaGetLastError();
 }
 

@@ -1,4 +1,5 @@
-// Paired float32 arithmetic and the hardware approximations.
+// Paired float32 arithmetic, the hardware approximations, and asynchronous
+// copies to shared memory.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -73,5 +74,21 @@ __device__ __forceinline__ uint32_t pack_bf16(F2 a)
     const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+
+// ---------------------------------------------------------------- copies global -> shared
+// BYTES = 16, 8 or 4 (both addresses aligned to it); `in` false: zeros.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void *to, const void *from, bool in)
+{
+    const uint32_t dst = static_cast<uint32_t>(__cvta_generic_to_shared(to));
+    const int n = in ? BYTES : 0;
+    if constexpr (BYTES == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(from), "r"(n) : "memory");
+    else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(from), "r"(n), "n"(BYTES) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 }  // namespace ssd
