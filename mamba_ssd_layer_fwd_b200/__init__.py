@@ -109,6 +109,8 @@ def library_path() -> str:
 def library():
     """Load libssd_b200.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -598,23 +600,31 @@ def _dtype_code(dtype) -> int:
     return 1 if dtype == torch.bfloat16 else 0
 
 
-class _on_device:
-    """Makes `dev` the current device for a call, where it is not."""
+def _call(dev, fn, *args):
+    """fn(*args) with `dev` as the current device."""
+    import torch
+    if dev.index == torch._C._cuda_getDevice():
+        return fn(*args)
+    with torch.cuda.device(dev):
+        return fn(*args)
 
-    def __init__(self, dev):
-        import torch
-        index = dev.index
-        self._guard = None
-        if index is not None and index != torch.cuda.current_device():
-            self._guard = torch.cuda.device(dev)
 
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
+def _stream_of(stream, dev) -> int:
+    """Handle of `stream`, or of the stream that is current on `dev`."""
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev.index) if stream is None else int(stream.cuda_stream)
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+
+def _need(name, t, dev, dtype, shape):
+    """As _check, for a tensor that is there: the checks that a decoding loop makes for every token."""
+    if t.dtype != dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _check(name, t, dev, dtype, tuple(shape))
+
+
+def _new(x):
+    """Uninitialised contiguous tensor like x."""
+    import torch
+    return torch.empty_like(x) if x.is_contiguous() else x.new_empty(x.shape)
 
 
 def _workspace(workspace, need, what, dev):
@@ -684,24 +694,23 @@ def ssd_glr_fwd(x, r, i, A_log, initial_states=None, cu_seqlens=None, return_fin
     p = _glr_params(x, nseq, cu_seqlens, torch.float32, strides)
     b, T, D = x.shape
     ref = ctypes.byref(p)
-    with _on_device(dev):
-        workspace = _workspace(workspace, lib.ssd_glr_fwd_workspace_size(ref), "ssd_glr_fwd_workspace_size", dev)
-        if y is None:
-            y = torch.empty((b, T, D), dtype=x.dtype, device=dev)
-        if return_final_states and final_states is None:
-            final_states = torch.empty((nseq, D), dtype=torch.float32, device=dev)
-        if return_chunk_states and chunk_states is None:
-            chunk_states = torch.empty((b, -(-T // GLR_CHUNK), D), dtype=torch.float32, device=dev)
-        st = _stream_handle(stream)
-        rc = lib.ssd_glr_fwd(ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states), _ptr(cu_seqlens),
-                             _ptr(y), _ptr(final_states), _ptr(chunk_states), _ptr(workspace),
-                             workspace.numel() * workspace.element_size(), st)
+    workspace = _workspace(workspace, lib.ssd_glr_fwd_workspace_size(ref), "ssd_glr_fwd_workspace_size", dev)
+    if y is None:
+        y = _new(x)
+    if return_final_states and final_states is None:
+        final_states = torch.empty((nseq, D), dtype=torch.float32, device=dev)
+    if return_chunk_states and chunk_states is None:
+        chunk_states = torch.empty((b, -(-T // GLR_CHUNK), D), dtype=torch.float32, device=dev)
+    st = _stream_of(stream, dev)
+    rc = _call(dev, lib.ssd_glr_fwd, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states),
+               _ptr(cu_seqlens), _ptr(y), _ptr(final_states), _ptr(chunk_states), _ptr(workspace),
+               workspace.numel() * workspace.element_size(), st)
+    if rc != 0:
+        raise SsdError(rc, "ssd_glr_fwd")
+    if check_status:
+        rc = _call(dev, lib.ssd_get_status, _ptr(workspace), st)
         if rc != 0:
-            raise SsdError(rc, "ssd_glr_fwd")
-        if check_status:
-            rc = lib.ssd_get_status(_ptr(workspace), st)
-            if rc != 0:
-                raise SsdError(rc, "ssd_glr_fwd (device status)")
+            raise SsdError(rc, "ssd_glr_fwd (device status)")
     out = (y,) + tuple(t for t in (final_states, chunk_states) if t is not None)
     return out if len(out) > 1 else y
 
@@ -728,23 +737,21 @@ def ssd_glr_bwd(x, r, i, A_log, dy, initial_states=None, cu_seqlens=None, dfinal
     p = _glr_params(x, nseq, cu_seqlens, gdt, strides)
     shape, D = tuple(x.shape), x.shape[2]
     ref = ctypes.byref(p)
-    with _on_device(dev):
-        need = lib.ssd_glr_bwd_workspace_size(ref, int(chunk_states is not None))
-        workspace = _workspace(workspace, need, "ssd_glr_bwd_workspace_size", dev)
-        dx, dr, di = (torch.empty(shape, dtype=gdt, device=dev) for _ in range(3))
-        dA_log = torch.empty(D, dtype=torch.float32, device=dev)
-        dinit = torch.empty((nseq, D), dtype=torch.float32, device=dev) if want_dinitial else None
-        st = _stream_handle(stream)
-        rc = lib.ssd_glr_bwd(ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states), _ptr(cu_seqlens),
-                             _ptr(chunk_states), _ptr(dy), _ptr(dfinal_states), _ptr(dx), _ptr(dr), _ptr(di),
-                             _ptr(dA_log), _ptr(dinit), _ptr(workspace),
-                             workspace.numel() * workspace.element_size(), st)
+    need = lib.ssd_glr_bwd_workspace_size(ref, int(chunk_states is not None))
+    workspace = _workspace(workspace, need, "ssd_glr_bwd_workspace_size", dev)
+    dx, dr, di = (torch.empty(shape, dtype=gdt, device=dev) for _ in range(3))
+    dA_log = torch.empty(D, dtype=torch.float32, device=dev)
+    dinit = torch.empty((nseq, D), dtype=torch.float32, device=dev) if want_dinitial else None
+    st = _stream_of(stream, dev)
+    rc = _call(dev, lib.ssd_glr_bwd, ref, _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(initial_states),
+               _ptr(cu_seqlens), _ptr(chunk_states), _ptr(dy), _ptr(dfinal_states), _ptr(dx), _ptr(dr), _ptr(di),
+               _ptr(dA_log), _ptr(dinit), _ptr(workspace), workspace.numel() * workspace.element_size(), st)
+    if rc != 0:
+        raise SsdError(rc, "ssd_glr_bwd")
+    if check_status:
+        rc = _call(dev, lib.ssd_get_status, _ptr(workspace), st)
         if rc != 0:
-            raise SsdError(rc, "ssd_glr_bwd")
-        if check_status:
-            rc = lib.ssd_get_status(_ptr(workspace), st)
-            if rc != 0:
-                raise SsdError(rc, "ssd_glr_bwd (device status)")
+            raise SsdError(rc, "ssd_glr_bwd (device status)")
     return {"dx": dx, "dr": dr, "di": di, "dA_log": dA_log, "dinitial_states": dinit}
 
 
@@ -757,9 +764,12 @@ def _validate_glr_step(x, r, i, A_log, state, y=None):
     dev, shape = x.device, x.shape
     strides = (_row_stride("x", x, dev, io, shape), _row_stride("r", r, dev, io, shape),
                _row_stride("i", i, dev, io, shape))
-    _check("A_log", A_log, dev, torch.float32, (shape[1],), required=True)
-    _check("state", state, dev, torch.float32, shape, required=True)
-    _check("y", y, dev, io, shape)
+    if A_log is None or state is None:
+        raise ValueError("A_log and state are required")
+    _need("A_log", A_log, dev, torch.float32, shape[1:])
+    _need("state", state, dev, torch.float32, shape)
+    if y is not None:
+        _need("y", y, dev, io, shape)
     return strides
 
 
@@ -768,7 +778,6 @@ def ssd_glr_step(x, r, i, A_log, state, y=None, stream=None):
     the C ABI; updates `state` (batch, channels) float32 in place and returns y.
     x, r, i (batch, channels) share the io dtype and may be column ranges of
     one tensor; A_log (channels,) is float32."""
-    import torch
     dev = x.device
     if dev.type != "cuda":
         raise ValueError("ssd_glr_step runs on CUDA tensors only")
@@ -776,11 +785,10 @@ def ssd_glr_step(x, r, i, A_log, state, y=None, stream=None):
     strides = _validate_glr_step(x, r, i, A_log, state, y)
     b, D = x.shape
     p = SsdGlrStepParams(b, D, _dtype_code(x.dtype), *strides)
-    with _on_device(dev):
-        if y is None:
-            y = torch.empty((b, D), dtype=x.dtype, device=dev)
-        rc = lib.ssd_glr_step(ctypes.byref(p), _ptr(x), _ptr(r), _ptr(i), _ptr(A_log), _ptr(state), _ptr(y),
-                              _stream_handle(stream))
+    if y is None:
+        y = _new(x)
+    rc = _call(dev, lib.ssd_glr_step, ctypes.byref(p), x.data_ptr(), r.data_ptr(), i.data_ptr(), A_log.data_ptr(),
+               state.data_ptr(), y.data_ptr(), _stream_of(stream, dev))
     if rc != 0:
         raise SsdError(rc, "ssd_glr_step")
     return y
@@ -801,10 +809,15 @@ def _validate_layer_norm(x, weight, bias=None, residual=None, z=None, ngroups=1,
         raise ValueError("residual and z exclude one another")
     xs = _row_stride("x", x, dev, io, shape)
     zs = D if z is None else _row_stride("z", z, dev, io, shape)
-    _check("residual", residual, dev, io, shape)
-    _check("weight", weight, dev, torch.float32, (D,), required=True)
-    _check("bias", bias, dev, torch.float32, (D,))
-    _check("y", y, dev, io, shape)
+    if weight is None:
+        raise ValueError("weight is required")
+    _need("weight", weight, dev, torch.float32, shape[-1:])
+    if bias is not None:
+        _need("bias", bias, dev, torch.float32, shape[-1:])
+    if residual is not None:
+        _need("residual", residual, dev, io, shape)
+    if y is not None:
+        _need("y", y, dev, io, shape)
     return x.numel() // D, D, xs, zs
 
 
@@ -829,16 +842,14 @@ def ssd_layer_norm_fwd(x, weight, bias=None, residual=None, z=None, ngroups: int
     code = _dtype_code(x.dtype)
     p = SsdLayerNormParams(rows, D, ngroups, eps, code, code, xs, zs)
     shape = tuple(x.shape)
-    with _on_device(dev):
-        if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=dev)
-        total = None if residual is None else torch.empty(shape, dtype=x.dtype, device=dev)
-        mean = rstd = None
-        if return_stats:
-            mean = torch.empty(shape[:-1] + (ngroups,), dtype=torch.float32, device=dev)
-            rstd = torch.empty(shape[:-1] + (ngroups,), dtype=torch.float32, device=dev)
-        rc = lib.ssd_layer_norm_fwd(ctypes.byref(p), _ptr(x), _ptr(residual), _ptr(z), _ptr(weight), _ptr(bias),
-                                    _ptr(y), _ptr(total), _ptr(mean), _ptr(rstd), _stream_handle(stream))
+    if y is None:
+        y = _new(x)
+    total = None if residual is None else _new(x)
+    mean = rstd = None
+    if return_stats:
+        mean, rstd = torch.empty((2, *shape[:-1], ngroups), dtype=torch.float32, device=dev).unbind(0)
+    rc = _call(dev, lib.ssd_layer_norm_fwd, ctypes.byref(p), x.data_ptr(), _ptr(residual), _ptr(z), weight.data_ptr(),
+               _ptr(bias), y.data_ptr(), _ptr(total), _ptr(mean), _ptr(rstd), _stream_of(stream, dev))
     if rc != 0:
         raise SsdError(rc, "ssd_layer_norm_fwd")
     out = (y,) + tuple(t for t in (total, mean, rstd) if t is not None)
@@ -880,16 +891,15 @@ def ssd_layer_norm_bwd(x, weight, dy, mean, rstd, z=None, dresidual=None, ngroup
                                                     workspace)
     p = SsdLayerNormParams(rows, D, ngroups, 0.0, _dtype_code(x.dtype), _dtype_code(gdt), xs, zs)
     ref, shape = ctypes.byref(p), tuple(x.shape)
-    with _on_device(dev):
-        workspace = _workspace(workspace, lib.ssd_layer_norm_bwd_workspace_size(ref),
-                               "ssd_layer_norm_bwd_workspace_size", dev)
-        dx = torch.empty(shape, dtype=gdt, device=dev)
-        dz = None if z is None else torch.empty(shape, dtype=gdt, device=dev)
-        dw = torch.empty(D, dtype=torch.float32, device=dev)
-        db = torch.empty(D, dtype=torch.float32, device=dev)
-        rc = lib.ssd_layer_norm_bwd(ref, _ptr(x), _ptr(z), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
-                                    _ptr(dresidual), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(workspace),
-                                    workspace.numel() * workspace.element_size(), _stream_handle(stream))
+    workspace = _workspace(workspace, _call(dev, lib.ssd_layer_norm_bwd_workspace_size, ref),
+                           "ssd_layer_norm_bwd_workspace_size", dev)
+    dx = torch.empty(shape, dtype=gdt, device=dev)
+    dz = None if z is None else torch.empty(shape, dtype=gdt, device=dev)
+    dw = torch.empty(D, dtype=torch.float32, device=dev)
+    db = torch.empty(D, dtype=torch.float32, device=dev)
+    rc = _call(dev, lib.ssd_layer_norm_bwd, ref, _ptr(x), _ptr(z), _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dy),
+               _ptr(dresidual), _ptr(dx), _ptr(dz), _ptr(dw), _ptr(db), _ptr(workspace),
+               workspace.numel() * workspace.element_size(), _stream_of(stream, dev))
     if rc != 0:
         raise SsdError(rc, "ssd_layer_norm_bwd")
     return {"dx": dx, "dz": dz, "dweight": dw, "dbias": db}
