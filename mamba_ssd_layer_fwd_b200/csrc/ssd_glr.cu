@@ -13,10 +13,10 @@
 // Tiles of one row wait for earlier tiles' maps.  Work is handed out by a
 // ticket, earlier tiles first, and a tile publishes its own map before it
 // waits, so a wait only ever concerns CTAs that already run.  The state
-// entering tile k is built from the state after the last whole group of
-// kGroup tiles, published by that group's last tile, and the maps of the tiles
-// since, always in the same order: results do not depend on timing, and the
-// chain of dependent waits is ntiles / kGroup long.
+// entering tile k is built from the state after the last whole group of GROUP
+// tiles, published by that group's last tile, and the maps of the tiles since,
+// always in the same order: results do not depend on timing, and the chain of
+// dependent waits is ntiles / GROUP long.
 #include <algorithm>
 #include <atomic>
 #include <initializer_list>
@@ -32,7 +32,6 @@
 namespace ssd {
 namespace {
 
-constexpr int kGroup = 16;          // tiles between two published states
 
 // Work split of one call (host and device).
 struct Tiling {
@@ -41,6 +40,8 @@ struct Tiling {
     float4 *maps;                   // [row][tile][nblk * 32]: of channel pairs
     float2 *states;                 // [row][group][nblk * 32]
 };
+
+__host__ __device__ __forceinline__ int groups_of(const Tiling &tl, int group) { return (tl.ntiles + group - 1) / group; }
 
 // The row's position of the CTA's tile, counted along the direction of the scan.
 struct Item {
@@ -121,18 +122,18 @@ __device__ __forceinline__ F2 map_B(float4 m) { return f2(m.z, m.w); }
 
 struct Exchange {
     float4 run[kRuns][32];          // maps of the tile's runs, in scan order, by channel pair
-    float4 tile[kWarps][32];        // maps of the group's earlier tiles, kGroup / kWarps at a time
+    float4 tile[kWarps][32];        // maps of the group's earlier tiles, GROUP / kWarps at a time
     float2 state[32];               // state after the group before (in the first group: entering the row)
 };
 
 // A warp's share of the exchange between the tiles of a row, a channel pair a
-// lane: kGroup / kWarps of the group's earlier tiles' maps, whose composition
+// lane: GROUP / kWarps of the group's earlier tiles' maps, whose composition
 // it leaves in ex.tile; the last warp also has the state after the group
 // before.  ask() sends for them, finish() waits until all are there: the round
 // trip to L2 passes while the tile's own maps are composed.
-template <bool PACKED>
+template <int GROUP, bool PACKED>
 struct Gather {
-    static constexpr int N = kGroup / kWarps;
+    static constexpr int N = GROUP / kWarps;
     const float4 *maps;
     const float2 *before;
     uint4 m[N];
@@ -151,12 +152,12 @@ struct Gather {
 
     __device__ __forceinline__ void ask(const Tiling &tl, const Item &it, int w, int lane)
     {
-        const int in_group = it.step % kGroup, group = it.step / kGroup, pair = it.blk * 32 + lane;
+        const int in_group = it.step % GROUP, group = it.step / GROUP, pair = it.blk * 32 + lane;
         stride = tl.nblk * 32;
         cnt = min(max(in_group - w * N, 0), N);
         state = w == kWarps - 1 && group > 0;
-        maps = &tl.maps[((long long)it.row * tl.ntiles + group * kGroup + w * N) * stride + pair];
-        before = &tl.states[((long long)it.row * ((tl.ntiles + kGroup - 1) / kGroup) + group - 1) * stride + pair];
+        maps = &tl.maps[((long long)it.row * tl.ntiles + group * GROUP + w * N) * stride + pair];
+        before = &tl.states[((long long)it.row * groups_of(tl, GROUP) + group - 1) * stride + pair];
         peek_all();
     }
 
@@ -213,14 +214,14 @@ __device__ __forceinline__ Map4 runs_before(const float4 (&maps)[kRuns][32], int
 }
 
 // The state that enters the tile, of a lane's channels (after gather_maps and a barrier).
-template <bool PACKED>
+template <int GROUP, bool PACKED>
 __device__ __forceinline__ F4 enter_tile(const Exchange &ex, int in_group, int quad)
 {
     const float4 v = *reinterpret_cast<const float4 *>(&ex.state[2 * quad]);
     F4 h = {f2(v.x, v.y), f2(v.z, v.w)};
 #pragma unroll
     for (int k = 0; k < kWarps; ++k)
-        if (k * (kGroup / kWarps) < in_group)
+        if (k * (GROUP / kWarps) < in_group)
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 const float4 m = ex.tile[k][2 * quad + p];
@@ -230,10 +231,10 @@ __device__ __forceinline__ F4 enter_tile(const Exchange &ex, int in_group, int q
 }
 
 // The lanes of the scan's last run publish the tile's map ...
-template <bool PACKED>
+template <int GROUP, bool PACKED>
 __device__ __forceinline__ void post_map(const Tiling &tl, const Item &it, const Map4 &before, const Exchange &ex, int quad)
 {
-    if (it.step + 1 >= tl.ntiles || it.step % kGroup == kGroup - 1) return;     // nobody reads it
+    if (it.step + 1 >= tl.ntiles || it.step % GROUP == GROUP - 1) return;       // nobody reads it
     float4 *to = &tl.maps[(((long long)it.row * tl.ntiles + it.step) * tl.nblk + it.blk) * 32 + 2 * quad];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
@@ -244,13 +245,12 @@ __device__ __forceinline__ void post_map(const Tiling &tl, const Item &it, const
     }
 }
 // ... and, for a group's last tile, the state after it (h: entering the run).
-template <bool PACKED>
+template <int GROUP, bool PACKED>
 __device__ __forceinline__ void post_state(const Tiling &tl, const Item &it, F4 h, const Exchange &ex, int quad, int *status)
 {
-    if (it.step + 1 >= tl.ntiles || it.step % kGroup != kGroup - 1) return;
+    if (it.step + 1 >= tl.ntiles || it.step % GROUP != GROUP - 1) return;
     if (*reinterpret_cast<volatile int *>(status) == kDevTimeout) return;
-    const int groups = (tl.ntiles + kGroup - 1) / kGroup;
-    float2 *to = &tl.states[(((long long)it.row * groups + it.step / kGroup) * tl.nblk + it.blk) * 32 + 2 * quad];
+    float2 *to = &tl.states[(((long long)it.row * groups_of(tl, GROUP) + it.step / GROUP) * tl.nblk + it.blk) * 32 + 2 * quad];
 #pragma unroll
     for (int p = 0; p < 2; ++p) {
         const float4 v = ex.run[kRuns - 1][2 * quad + p];
@@ -322,7 +322,7 @@ __device__ __forceinline__ int4 slot_of(const Tiling &tl, int ticket, int total)
 // drawn while this one's gates are computed, and each warp copies its runs of
 // the next tile as soon as its own are in registers, so HBM reads go on while
 // the CTA waits for other tiles and writes.
-template <typename T, int COPY, bool PACKED>
+template <typename T, int COPY, int GROUP, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 4)
 glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *__restrict__ y,
                float *__restrict__ final_states, float *__restrict__ chunk_states)
@@ -426,7 +426,7 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
                     for (int p = 0; p < 2; ++p) b[j].p[p] = fma(a[j].p[p], h0.p[p], b[j].p[p]), a[j].p[p] = f2(0.0f);
                 }
         }
-        Gather<PACKED> others;
+        Gather<GROUP, PACKED> others;
         others.ask(tl, it, w, lane);
 #pragma unroll
         for (int p = 0; p < 2; ++p) {
@@ -438,14 +438,14 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
         __syncthreads();
         const Map4 before = runs_before<PACKED>(sm.ex.run, run, quad);
-        if (run == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
+        if (run == kRuns - 1) post_map<GROUP, PACKED>(tl, it, before, sm.ex, quad);
         fetch(sm.slot[(n + 1) & 1]);
         others.finish(it, w, lane, !PACKED && g.init ? g.init + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
         __syncthreads();
-        F4 h = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
+        F4 h = enter_tile<GROUP, PACKED>(sm.ex, it.step % GROUP, quad);
 #pragma unroll
         for (int p = 0; p < 2; ++p) h.p[p] = apply_map<PACKED>(before.A[p], before.B[p], h.p[p]);
-        if (run == kRuns - 1) post_state<PACKED>(tl, it, h, sm.ex, quad, g.status);
+        if (run == kRuns - 1) post_state<GROUP, PACKED>(tl, it, h, sm.ex, quad, g.status);
         if (!live || t0 >= g.T) continue;
 
         if (chunk_states && run == 0) {
@@ -481,27 +481,37 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
 }
 
 template <typename T> struct BwdSmem {
-    static constexpr int kStages = sizeof(T) == 2 ? 2 : 1;
-    T in[kStages][4][kTile][64];    // r, i, x, dy
+    union {
+        T in[3][kTile][64];             // r, i, x; once they are in registers:
+        float4 kept[3][kTile][16];      // what the gradients need of each element, four channels a lane
+    };
+    T dy[kTile][64];
     uint64_t full;
     int abort;
-    Exchange ex;                    // of the scan backwards: its runs are in reverse
-    float4 run[kRuns][32];          // maps of the forward scan's runs, later dA_log's sums by warp
-    float2 state[32];               // state that enters the tile
+    Exchange ex;                        // of the scan backwards: its runs are in reverse
+    float4 run[kRuns][32];              // maps of the forward scan's runs, later dA_log's sums by warp
+    float2 state[32];                   // state that enters the tile
     int4 slot[2];
 };
 
 // The row's last tile first.  The states come from the chunk state and the runs'
 // maps; the gradient that enters a token from the later ones, c_t = a_t (dy_t +
 // c_{t+1}), is a map of the same kind scanned backwards, so the exchange between
-// tiles is the forward's.  1 - a and the state before each token stay in
-// registers over it (so a is off by up to 2^-24 here, not by 2^-24 of itself:
-// gradients and recomputed states by that much of the value that is decayed);
-// the other gates are taken anew from the staged inputs (17 instructions an
-// element, against six more registers an element and half the warps).
+// tiles is the forward's.
+//
+// With g the whole gradient of a state, an element's results are
+//     dx = g P,   di = g Q,   dq q = g U,   dr = g U sigmoid(-r),   c = g a
+// P = m sigmoid(i), Q = P x sigmoid(-i), U = q a (a / m sigmoid(i) x - h).  The
+// state before the token is h = A H + B, (A, B) the map of the run's tokens
+// before it and H the state that enters the run, so U = U1 - U2 H with U1 and U2
+// known before H is: the gates are evaluated once.  a, U1 and U2 stay in
+// registers over the exchange (96 of them), P, Q and sigmoid(-r) in shared
+// memory, where the tile's inputs were.  (Evaluating the gates again instead
+// cost 83 instructions an element against 58, and 0.37 ms against 0.27 ms on 8 x
+// 2048 x 5120 in bf16.)
 //
 // part: dA_log's sums of each tile, [row][tile][channels].
-template <typename T, typename G, int COPY, bool PACKED>
+template <typename T, typename G, int COPY, int GROUP, bool PACKED>
 __global__ void __launch_bounds__(kThreads, 3)
 glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, const float *__restrict__ chunk_states,
                const T *__restrict__ dy, const float *__restrict__ dfinal, G *__restrict__ dx, G *__restrict__ dr,
@@ -511,31 +521,29 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
     BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(smem_raw);
     __shared__ Marks<PACKED ? kTile : 1> marks;
     constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
-    constexpr int kStages = BwdSmem<T>::kStages;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int back = kRuns - 1 - run;                       // the run in the order of the scan
     const int total = tl.rows * tl.ntiles * tl.nblk;
 
-    const auto fetch = [&](int4 it, int stage) {
+    const auto fetch = [&](int4 it) {
         const int c0 = it.z * 64, tile0 = (tl.ntiles - 1 - it.y) * kTile;
         if constexpr (COPY == 16) {
             if (threadIdx.x == 0 && it.w) {
                 const int t = it.x * g.T + tile0;
-                tc::mbar_arrive_expect_tx(&sm.full, sizeof(sm.in[0]));
-                tc::tma_load_2d(sm.in[stage][0], &maps.r, &sm.full, c0, t);
-                tc::tma_load_2d(sm.in[stage][1], &maps.i, &sm.full, c0, t);
-                tc::tma_load_2d(sm.in[stage][2], &maps.x, &sm.full, c0, t);
-                tc::tma_load_2d(sm.in[stage][3], &maps.dy, &sm.full, c0, t);
+                tc::mbar_arrive_expect_tx(&sm.full, sizeof(sm.in) + sizeof(sm.dy));
+                tc::tma_load_2d(sm.in[0], &maps.r, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[1], &maps.i, &sm.full, c0, t);
+                tc::tma_load_2d(sm.in[2], &maps.x, &sm.full, c0, t);
+                tc::tma_load_2d(sm.dy, &maps.dy, &sm.full, c0, t);
             }
         } else {
             if (it.w) {
                 const int q0 = w * 2 * kL, t0 = tile0 + q0;
                 const long long row0 = (long long)it.x * g.T;
-                T(*in)[kTile][64] = sm.in[stage];
-                stage_runs<T, COPY>(in[0][q0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
-                stage_runs<T, COPY>(in[1][q0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
-                stage_runs<T, COPY>(in[2][q0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
-                stage_runs<T, COPY>(in[3][q0], dy + row0 * g.D, g.D, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.in[0][q0], static_cast<const T *>(g.r) + row0 * g.rs, g.rs, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.in[1][q0], static_cast<const T *>(g.i) + row0 * g.is, g.is, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.in[2][q0], static_cast<const T *>(g.x) + row0 * g.xs, g.xs, t0, g.T, c0, g.D, lane);
+                stage_runs<T, COPY>(sm.dy[q0], dy + row0 * g.D, g.D, t0, g.T, c0, g.D, lane);
             }
             copy_commit();
         }
@@ -550,13 +558,12 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         }
     }
     __syncthreads();
-    if (kStages == 2) fetch(sm.slot[0], 0);
+    fetch(sm.slot[0]);
 
     for (int n = 0;; ++n) {
         const int4 s4 = sm.slot[n & 1];
         if (!s4.w) break;
         const Item it{s4.x, s4.y, s4.z};
-        const int stage = n % kStages;
         int next = 0;
         if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
         const int tile = tl.ntiles - 1 - it.step, c = it.blk * 64 + 4 * quad, t0 = tile * kTile + run * kL, nc = g.D - c;
@@ -570,17 +577,6 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (cp < g.D) h0.x = from[0];
             if (cp + 1 < g.D) h0.y = from[1];
         }
-        if constexpr (kStages == 1) {
-            __syncthreads();                        // every warp is done with the tile before
-            fetch(s4, 0);
-        }
-        if constexpr (COPY == 16) {
-            if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
-        } else {
-            copy_wait<0>();
-        }
-        __syncthreads();
-        if (w == 0) sm.state[lane] = h0;
         RunMarks rm{0, 0};
         if constexpr (PACKED) {
             mark_sequences(g, marks, tile * kTile, (long long)it.step * tl.nblk + it.blk,
@@ -591,6 +587,22 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
                            });
             rm = run_marks(marks, run, lane);
         }
+        if constexpr (COPY == 16) {
+            if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
+        } else {
+            copy_wait<0>();
+            __syncwarp();
+        }
+        typename Raw4<T>::type rr[kL], ir[kL], xr[kL];
+#pragma unroll
+        for (int j = 0; j < kL; ++j) {
+            const int row = run * kL + j;
+            rr[j] = load_raw4(&sm.in[0][row][4 * quad]);
+            ir[j] = load_raw4(&sm.in[1][row][4 * quad]);
+            xr[j] = load_raw4(&sm.in[2][row][4 * quad]);
+        }
+        __syncthreads();                            // the tile's r, i and x are in registers
+        if (w == 0) sm.state[lane] = h0;
         const auto ex = [](float v) { return expf(v); };
         rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
         // a sequence's initial state, or the gradient of its final state, of the lane's channels
@@ -599,139 +611,143 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (p && live) v = load4_global<ALIGN>(p + (long long)s * g.D + c, nc);
             return v;
         };
-        const T(*in)[kTile][64] = sm.in[stage];
         const bool tail = t0 + kL > g.T;
 
-        F4 e[kL], b[kL];
-#pragma unroll
-        for (int j = 0; j < kL; ++j) {
-            const int row = run * kL + j;
-            const F4 r4 = load_gates(&in[0][row][4 * quad]), i4 = load_gates(&in[1][row][4 * quad]), x4 = load4(&in[2][row][4 * quad]);
-#pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
-                e[j].p[p] = decay2(k.q).e;
-                b[j].p[p] = mul(mul(scale2(e[j].p[p], decay_of(e[j].p[p])).m, k.si), x4.p[p]);
-            }
-        }
-        if (tail) {                                 // behind the row's end: state and gradient stay
-#pragma unroll
-            for (int j = 0; j < kL; ++j)
-                if (t0 + j >= g.T)
-#pragma unroll
-                    for (int p = 0; p < 2; ++p) e[j].p[p] = b[j].p[p] = f2(0.0f);
-        }
-        Gather<PACKED> others;
-        others.ask(tl, it, w, lane);
+        F4 a[kL], u1[kL], u2[kL];
         {
             F2 A[2], B[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) A[p] = f2(1.0f), B[p] = f2(0.0f);
+            const auto gates = [&](auto tail_tag) {
+                constexpr bool TAIL = decltype(tail_tag)::value;
 #pragma unroll
-            for (int j = 0; j < kL; ++j) {
-                F4 fa, fb = b[j];
+                for (int j = 0; j < kL; ++j) {
+                    const int row = run * kL + j;
+                    const F4 r4 = gates_of(rr[j]), i4 = gates_of(ir[j]), x4 = values_of(xr[j]);
+                    if (PACKED && (rm.first >> j & 1)) {    // the state before it is known
+                        const F4 v = of_sequence(g.init, marks.first[row]);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) fa.p[p] = decay_of(e[j].p[p]);
-                if (PACKED && (rm.first >> j & 1)) {
-                    const F4 v = of_sequence(g.init, marks.first[run * kL + j]);
+                        for (int p = 0; p < 2; ++p) A[p] = f2(0.0f), B[p] = v.p[p];
+                    }
+                    F4 P, Q, O;
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) fb.p[p] = fma(fa.p[p], v.p[p], fb.p[p]), fa.p[p] = f2(0.0f);
+                    for (int p = 0; p < 2; ++p) {
+                        const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
+                        Decay2 d = decay2(k.q);
+                        const Scale2 sc = scale2(d.e, d.a);
+                        P.p[p] = mul(sc.m, k.si);
+                        F2 b = mul(P.p[p], x4.p[p]);
+                        Q.p[p] = mul(b, k.osi);
+                        O.p[p] = k.osr;
+                        // q a (a / m) sigmoid(i) x, with q / m finite as q -> 0
+                        const F2 s = mul(k.q, d.a);
+                        const F2 gain = mul(mul(s, d.a), mul(mul(sc.inv_m, k.si), x4.p[p]));
+                        u1[j].p[p] = fma(mul(s, f2(-1.0f)), B[p], gain);
+                        u2[j].p[p] = mul(s, A[p]);
+                        if (TAIL && t0 + j >= g.T) d.a = f2(1.0f), b = f2(0.0f);    // behind the row's end: nothing changes
+                        a[j].p[p] = d.a;
+                        B[p] = fma(d.a, B[p], b);
+                        A[p] = mul(A[p], d.a);
+                    }
+                    sm.kept[0][row][quad] = quad_of(P);
+                    sm.kept[1][row][quad] = quad_of(Q);
+                    sm.kept[2][row][quad] = quad_of(O);
                 }
+            };
+            if (tail) gates(std::true_type());
+            else gates(std::false_type());
+            Gather<GROUP, PACKED> others;
+            others.ask(tl, it, w, lane);
 #pragma unroll
-                for (int p = 0; p < 2; ++p) compose_map<PACKED>(A[p], B[p], fa.p[p], fb.p[p]);
+            for (int p = 0; p < 2; ++p) {
+                sm.run[run][2 * quad + p] = pack_map(A[p], B[p]);
+                if (PACKED) A[p] = f2(1.0f);
+                B[p] = f2(0.0f);
             }
 #pragma unroll
-            for (int p = 0; p < 2; ++p) sm.run[run][2 * quad + p] = pack_map(A[p], B[p]), A[p] = f2(1.0f), B[p] = f2(0.0f);
-#pragma unroll
             for (int j = kL - 1; j >= 0; --j) {
-                F4 gy = load4(&in[3][run * kL + j][4 * quad]);
+                F4 gy = load4(&sm.dy[run * kL + j][4 * quad]);
                 if (tail && t0 + j >= g.T) gy = {f2(0.0f), f2(0.0f)};
                 const bool last = PACKED && (rm.last >> j & 1);
                 if (last) {
                     const F4 v = of_sequence(dfinal, marks.last[run * kL + j]);
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) gy.p[p] = add(gy.p[p], v.p[p]);
+                    for (int p = 0; p < 2; ++p) gy.p[p] = add(gy.p[p], v.p[p]), A[p] = B[p] = f2(0.0f);
                 }
 #pragma unroll
                 for (int p = 0; p < 2; ++p) {
-                    const F2 a = decay_of(e[j].p[p]);
-                    compose_map<PACKED>(A[p], B[p], last ? f2(0.0f) : a, mul(a, gy.p[p]));
+                    B[p] = mul(a[j].p[p], add(gy.p[p], B[p]));
+                    if (PACKED) A[p] = mul(A[p], a[j].p[p]);    // otherwise the run's decay, as forwards
                 }
             }
 #pragma unroll
             for (int p = 0; p < 2; ++p) sm.ex.run[back][2 * quad + p] = pack_map(A[p], B[p]);
-        }
-        if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
-        __syncthreads();
-        const Map4 before = runs_before<PACKED>(sm.ex.run, back, quad);
-        if (back == kRuns - 1) post_map<PACKED>(tl, it, before, sm.ex, quad);
-        if (kStages == 2) fetch(sm.slot[(n + 1) & 1], (n + 1) & 1);
-        F4 h;
-        {
-            const Map4 m = runs_before<PACKED>(sm.run, run, quad);
-            const float4 v = *reinterpret_cast<const float4 *>(&sm.state[2 * quad]);
-            h.p[0] = apply_map<PACKED>(m.A[0], m.B[0], f2(v.x, v.y));
-            h.p[1] = apply_map<PACKED>(m.A[1], m.B[1], f2(v.z, v.w));
-        }
+            if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
+            __syncthreads();
+            const Map4 before = runs_before<PACKED>(sm.ex.run, back, quad);
+            if (back == kRuns - 1) post_map<GROUP, PACKED>(tl, it, before, sm.ex, quad);
+            {
+                const Map4 m = runs_before<PACKED>(sm.run, run, quad);
+                const float4 v = *reinterpret_cast<const float4 *>(&sm.state[2 * quad]);
+                const F2 h[2] = {apply_map<PACKED>(m.A[0], m.B[0], f2(v.x, v.y)),
+                                 apply_map<PACKED>(m.A[1], m.B[1], f2(v.z, v.w))};
 #pragma unroll
-        for (int j = 0; j < kL; ++j) {              // b[j] <- the state before token j
-            if (PACKED && (rm.first >> j & 1)) h = of_sequence(g.init, marks.first[run * kL + j]);
+                for (int j = 0; j < kL; ++j)        // u1 <- u1 - u2 h
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const F2 after = fma(decay_of(e[j].p[p]), h.p[p], b[j].p[p]);
-                b[j].p[p] = h.p[p];
-                h.p[p] = after;
+                    for (int p = 0; p < 2; ++p)
+                        u1[j].p[p] = apply_map<PACKED>(mul(u2[j].p[p], f2(-1.0f)), u1[j].p[p], h[p]);
             }
-        }
-        others.finish(it, w, lane, !PACKED && dfinal ? dfinal + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
-        __syncthreads();
-        F4 carry = enter_tile<PACKED>(sm.ex, it.step % kGroup, quad);
+            others.finish(it, w, lane, !PACKED && dfinal ? dfinal + (long long)it.row * g.D : nullptr, g.D, sm.ex, g.status);
+            __syncthreads();
+            F4 carry = enter_tile<GROUP, PACKED>(sm.ex, it.step % GROUP, quad);
 #pragma unroll
-        for (int p = 0; p < 2; ++p) carry.p[p] = apply_map<PACKED>(before.A[p], before.B[p], carry.p[p]);
-        if (back == kRuns - 1) post_state<PACKED>(tl, it, carry, sm.ex, quad, g.status);
+            for (int p = 0; p < 2; ++p) carry.p[p] = apply_map<PACKED>(before.A[p], before.B[p], carry.p[p]);
+            if (back == kRuns - 1) post_state<GROUP, PACKED>(tl, it, carry, sm.ex, quad, g.status);
 
-        F4 sum = {f2(0.0f), f2(0.0f)};
-        long long at = ((long long)it.row * g.T + t0 + kL - 1) * g.D + c;
+            F4 sum = {f2(0.0f), f2(0.0f)};
+            long long at = ((long long)it.row * g.T + t0 + kL - 1) * g.D + c;
+            const auto gradients = [&](auto tail_tag) {
+                constexpr bool TAIL = decltype(tail_tag)::value;
 #pragma unroll
-        for (int j = kL - 1; j >= 0; --j, at -= g.D) {
-            if (tail && t0 + j >= g.T) continue;
-            const int row = run * kL + j;
-            const F4 r4 = load_gates(&in[0][row][4 * quad]), i4 = load_gates(&in[1][row][4 * quad]);
-            const F4 x4 = load4(&in[2][row][4 * quad]);
-            F4 gy = load4(&in[3][row][4 * quad]);
-            if (PACKED && (rm.last >> j & 1)) carry = of_sequence(dfinal, marks.last[row]);
-            F4 ox, oi, orr;
+                for (int j = kL - 1; j >= 0; --j, at -= g.D) {
+                    if (TAIL && t0 + j >= g.T) continue;
+                    const int row = run * kL + j;
+                    const F4 P = values_of(sm.kept[0][row][quad]), Q = values_of(sm.kept[1][row][quad]);
+                    const F4 O = values_of(sm.kept[2][row][quad]);
+                    const F4 gy = load4(&sm.dy[row][4 * quad]);
+                    if (PACKED && (rm.last >> j & 1)) carry = of_sequence(dfinal, marks.last[row]);
+                    F4 ox, oi, orr;
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
-                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
-                const F2 a = decay_of(e[j].p[p]);
-                const Scale2 sc = scale2(e[j].p[p], a);
-                const F2 gt = add(gy.p[p], carry.p[p]), gs = mul(gt, k.si), ga = mul(gt, a);
-                ox.p[p] = mul(gs, sc.m);
-                oi.p[p] = mul(mul(ox.p[p], x4.p[p]), k.osi);
-                // q (a^2 / m) gs x - q a g h, with q / m finite as q -> 0
-                const F2 t = mul(mul(a, sc.inv_m), mul(gs, x4.p[p]));
-                const F2 dqq = mul(k.q, fma(a, t, mul(ga, mul(b[j].p[p], f2(-1.0f)))));
-                orr.p[p] = mul(dqq, k.osr);
-                sum.p[p] = add(sum.p[p], dqq);
-                carry.p[p] = ga;
-            }
-            if (live) {
-                store4<ALIGN>(dx + at, ox, nc);
-                store4<ALIGN>(di + at, oi, nc);
-                store4<ALIGN>(dr + at, orr, nc);
-                if (dinit) {
-                    const int s = PACKED ? (rm.first >> j & 1 ? marks.first[row] : -1) : (t0 + j == 0 ? it.row : -1);
-                    if (s >= 0) store4<ALIGN>(dinit + (long long)s * g.D + c, carry, nc);
+                    for (int p = 0; p < 2; ++p) {
+                        const F2 gt = add(gy.p[p], carry.p[p]), dqq = mul(gt, u1[j].p[p]);
+                        ox.p[p] = mul(gt, P.p[p]);
+                        oi.p[p] = mul(gt, Q.p[p]);
+                        orr.p[p] = mul(dqq, O.p[p]);
+                        sum.p[p] = add(sum.p[p], dqq);
+                        carry.p[p] = mul(gt, a[j].p[p]);
+                    }
+                    if (live) {
+                        store4<ALIGN>(dx + at, ox, nc);
+                        store4<ALIGN>(di + at, oi, nc);
+                        store4<ALIGN>(dr + at, orr, nc);
+                        if (dinit) {
+                            const int s = PACKED ? (rm.first >> j & 1 ? marks.first[row] : -1) : (j == 0 && t0 == 0 ? it.row : -1);
+                            if (s >= 0) store4<ALIGN>(dinit + (long long)s * g.D + c, carry, nc);
+                        }
+                    }
                 }
-            }
+            };
+            if (tail) gradients(std::true_type());
+            else gradients(std::false_type());
+            float4 v = quad_of(sum);
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
+            v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
+            if (half == 0) sm.run[0][w * 16 + quad] = v;
         }
-        float4 v;
-        split(sum.p[0], v.x, v.y), split(sum.p[1], v.z, v.w);
-        v.x += __shfl_xor_sync(0xffffffffu, v.x, 16), v.y += __shfl_xor_sync(0xffffffffu, v.y, 16);
-        v.z += __shfl_xor_sync(0xffffffffu, v.z, 16), v.w += __shfl_xor_sync(0xffffffffu, v.w, 16);
-        if (half == 0) sm.run[0][w * 16 + quad] = v;
-        __syncthreads();
+        // the copies that come next write where threads have written
+        if constexpr (COPY == 16) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncthreads();                            // every warp is done with the tile
+        fetch(sm.slot[(n + 1) & 1]);
         if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) {
             const float *col = &sm.run[0][0].x + threadIdx.x;
             part[((long long)it.row * tl.ntiles + tile) * g.D + it.blk * 64 + threadIdx.x] =
@@ -838,6 +854,27 @@ GlrArgs args_of(const ssd_glr_params &p, const void *x, const void *r, const voi
     return g;
 }
 
+int sm_count()
+{
+    static std::atomic<int> cache[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
+    int n = cache[dev].load(std::memory_order_relaxed);
+    if (n == 0) {
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
+        cache[dev].store(n, std::memory_order_relaxed);
+    }
+    return n;
+}
+
+// Tiles of a group.  Where the SMs have a channel block of a row each, a tile is
+// drawn about when the one before it is done, and short groups cost the fewest
+// maps (8 x 2048 x 5120 bf16: 0.149 ms against 0.161 with 16); with fewer
+// blocks many tiles of a row are in work at once and what counts is that the
+// chain of states is short (16384 x 2048 bf16: 0.101 ms against 0.118).
+constexpr int kShortGroup = 4, kLongGroup = 16;
+int group_of(const Tiling &t) { return t.rows * t.nblk >= sm_count() ? kShortGroup : kLongGroup; }
+
 // Workspace of one scan: status word, ticket counter, and the maps and states
 // that tiles hand on (all cleared before a call).
 struct Scan {
@@ -858,7 +895,7 @@ Scan scan_of(const ssd_glr_params &p, char *ws)
         t.maps = reinterpret_cast<float4 *>(ws + off);
         off = align_up(off + (size_t)t.rows * t.ntiles * t.nblk * 32 * sizeof(float4));
         t.states = reinterpret_cast<float2 *>(ws + off);
-        off = align_up(off + (size_t)t.rows * ((t.ntiles + kGroup - 1) / kGroup) * t.nblk * 32 * sizeof(float2));
+        off = align_up(off + (size_t)t.rows * groups_of(t, kShortGroup) * t.nblk * 32 * sizeof(float2));
     }
     s.bytes = off;
     return s;
@@ -878,19 +915,6 @@ BwdLayout bwd_layout(const ssd_glr_params &p, bool with_chunks)
     l.chunks = l.part + n;
     l.total = with_chunks ? l.chunks : l.chunks + n;
     return l;
-}
-
-int sm_count()
-{
-    static std::atomic<int> cache[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 148;
-    int n = cache[dev].load(std::memory_order_relaxed);
-    if (n == 0) {
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0) n = 148;
-        cache[dev].store(n, std::memory_order_relaxed);
-    }
-    return n;
 }
 
 // Bytes of one copy that the rows allow: 16, two elements or one.
@@ -934,10 +958,10 @@ bool encode_inputs(InputMaps &m, const ssd_glr_params &p, const GlrArgs &g, cons
            encode(m.x, g.x, p.io_dtype, n, g.D, g.xs) && (!dy || encode(m.dy, dy, p.io_dtype, n, g.D, g.D));
 }
 
-template <typename T, int COPY, bool PACKED>
+template <typename T, int COPY, int GROUP, bool PACKED>
 cudaError_t launch_fwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
 {
-    const auto kernel = glr_fwd_kernel<T, COPY, PACKED>;
+    const auto kernel = glr_fwd_kernel<T, COPY, GROUP, PACKED>;
     const int smem = sizeof(FwdSmem<T>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -950,14 +974,15 @@ cudaError_t launch_fwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl
 template <typename T>
 cudaError_t launch_fwd(const InputMaps &m, const GlrArgs &g, int copy, const Tiling &tl, void *y, float *fin, float *chunks, cudaStream_t st)
 {
-    constexpr int P = 2 * sizeof(T), S = sizeof(T);
-    if (g.cu)
-        return copy == 16  ? launch_fwd<T, 16, true>(m, g, tl, y, fin, chunks, st)
-               : copy == P ? launch_fwd<T, P, true>(m, g, tl, y, fin, chunks, st)
-                           : launch_fwd<T, S, true>(m, g, tl, y, fin, chunks, st);
-    return copy == 16  ? launch_fwd<T, 16, false>(m, g, tl, y, fin, chunks, st)
-           : copy == P ? launch_fwd<T, P, false>(m, g, tl, y, fin, chunks, st)
-                       : launch_fwd<T, S, false>(m, g, tl, y, fin, chunks, st);
+    constexpr int P = 2 * sizeof(T), S = sizeof(T), L = kLongGroup, M = kShortGroup;
+    const bool lng = group_of(tl) == kLongGroup;
+    if (copy == 16) {
+        if (g.cu) return lng ? launch_fwd<T, 16, L, true>(m, g, tl, y, fin, chunks, st) : launch_fwd<T, 16, M, true>(m, g, tl, y, fin, chunks, st);
+        return lng ? launch_fwd<T, 16, L, false>(m, g, tl, y, fin, chunks, st) : launch_fwd<T, 16, M, false>(m, g, tl, y, fin, chunks, st);
+    }
+    // rows that TMA cannot address: one length of groups
+    if (copy == P) return g.cu ? launch_fwd<T, P, L, true>(m, g, tl, y, fin, chunks, st) : launch_fwd<T, P, L, false>(m, g, tl, y, fin, chunks, st);
+    return g.cu ? launch_fwd<T, S, L, true>(m, g, tl, y, fin, chunks, st) : launch_fwd<T, S, L, false>(m, g, tl, y, fin, chunks, st);
 }
 
 cudaError_t run_copy(const GlrArgs &g, const float *from, float *to, cudaStream_t st)
@@ -990,10 +1015,10 @@ struct BwdArgs {
     float *part, *dA, *dinit;
 };
 
-template <typename T, typename G, int COPY, bool PACKED>
+template <typename T, typename G, int COPY, int GROUP, bool PACKED>
 cudaError_t launch_bwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
 {
-    const auto kernel = glr_bwd_kernel<T, G, COPY, PACKED>;
+    const auto kernel = glr_bwd_kernel<T, G, COPY, GROUP, PACKED>;
     const int smem = sizeof(BwdSmem<T>);
     const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -1009,14 +1034,15 @@ cudaError_t launch_bwd(const InputMaps &maps, const GlrArgs &g, const Tiling &tl
 template <typename T, typename G>
 cudaError_t launch_bwd(const InputMaps &m, const GlrArgs &g, int copy, const Tiling &tl, const BwdArgs &b, cudaStream_t st)
 {
-    constexpr int P = 2 * sizeof(T), S = sizeof(T);
-    if (g.cu)
-        return copy == 16  ? launch_bwd<T, G, 16, true>(m, g, tl, b, st)
-               : copy == P ? launch_bwd<T, G, P, true>(m, g, tl, b, st)
-                           : launch_bwd<T, G, S, true>(m, g, tl, b, st);
-    return copy == 16  ? launch_bwd<T, G, 16, false>(m, g, tl, b, st)
-           : copy == P ? launch_bwd<T, G, P, false>(m, g, tl, b, st)
-                       : launch_bwd<T, G, S, false>(m, g, tl, b, st);
+    constexpr int P = 2 * sizeof(T), S = sizeof(T), L = kLongGroup, M = kShortGroup;
+    const bool lng = group_of(tl) == kLongGroup;
+    if (copy == 16) {
+        if (g.cu) return lng ? launch_bwd<T, G, 16, L, true>(m, g, tl, b, st) : launch_bwd<T, G, 16, M, true>(m, g, tl, b, st);
+        return lng ? launch_bwd<T, G, 16, L, false>(m, g, tl, b, st) : launch_bwd<T, G, 16, M, false>(m, g, tl, b, st);
+    }
+    // rows that TMA cannot address: one length of groups
+    if (copy == P) return g.cu ? launch_bwd<T, G, P, L, true>(m, g, tl, b, st) : launch_bwd<T, G, P, L, false>(m, g, tl, b, st);
+    return g.cu ? launch_bwd<T, G, S, L, true>(m, g, tl, b, st) : launch_bwd<T, G, S, L, false>(m, g, tl, b, st);
 }
 
 }  // namespace

@@ -117,9 +117,6 @@ __device__ __forceinline__ Decay2 decay2(F2 q)
     const F2 v = mul(u, f), minus = f2(-1.0f), one = f2(1.0f);
     return {mul(s, fma(v, minus, one)), fma(s, v, fma(s, minus, one))};
 }
-// a from e alone, to half a step of 1
-__device__ __forceinline__ F2 decay_of(F2 e) { return fma(e, f2(-1.0f), f2(1.0f)); }
-
 // m = sqrt(1 - a^2) = sqrt(e (1 + a)) and 1 / m (finite at m = 0: the radicand is kept off 0)
 struct Scale2 {
     F2 m, inv_m;
@@ -140,38 +137,55 @@ struct F4 {
     F2 p[2];
 };
 
-__device__ __forceinline__ F4 load4(const float *p)         // 16-byte aligned
+// Four elements as they lie in memory.
+template <typename T> struct Raw4;
+template <> struct Raw4<float> {
+    typedef float4 type;
+};
+template <> struct Raw4<__nv_bfloat16> {
+    typedef uint2 type;
+};
+template <typename T>
+__device__ __forceinline__ typename Raw4<T>::type load_raw4(const T *p)      // aligned to four elements
 {
-    const float4 v = *reinterpret_cast<const float4 *>(p);
-    return {f2(v.x, v.y), f2(v.z, v.w)};
+    return *reinterpret_cast<const typename Raw4<T>::type *>(p);
 }
-__device__ __forceinline__ F4 load4(const __nv_bfloat16 *p) // 8-byte aligned
+__device__ __forceinline__ F4 values_of(float4 v) { return {f2(v.x, v.y), f2(v.z, v.w)}; }
+__device__ __forceinline__ F4 values_of(uint2 u)
 {
-    const uint2 u = *reinterpret_cast<const uint2 *>(p);
     return {f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
             f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))};
 }
+template <typename T>
+__device__ __forceinline__ F4 load4(const T *p) { return values_of(load_raw4(p)); }
 
 // Gate logits, at least -43 (NaN stays NaN): in bf16 two at a time.
-__device__ __forceinline__ F4 load_gates(const float *p)
+__device__ __forceinline__ F4 gates_of(float4 r)
 {
     const auto clamp = [](float v) {
         float o;
         asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(v), "f"(-43.0f));
         return o;
     };
-    F4 v = load4(p);
+    F4 v = values_of(r);
     v.p[0] = each(v.p[0], clamp), v.p[1] = each(v.p[1], clamp);
     return v;
 }
-__device__ __forceinline__ F4 load_gates(const __nv_bfloat16 *p)
+__device__ __forceinline__ F4 gates_of(uint2 u)
 {
-    uint2 u = *reinterpret_cast<const uint2 *>(p);
     constexpr uint32_t low = 0xc22cc22cu;           // -43, -43
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(u.x) : "r"(low));
     asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(u.y) : "r"(low));
-    return {f2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u)),
-            f2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u))};
+    return values_of(u);
+}
+template <typename T>
+__device__ __forceinline__ F4 load_gates(const T *p) { return gates_of(load_raw4(p)); }
+
+__device__ __forceinline__ float4 quad_of(const F4 &v)
+{
+    float4 o;
+    split(v.p[0], o.x, o.y), split(v.p[1], o.z, o.w);
+    return o;
 }
 
 template <int ALIGN>

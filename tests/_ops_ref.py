@@ -79,18 +79,6 @@ class Glr:
                 self.h[row, t], self.eh[row, t] = h, E + 16 * U * H
             self.final[k], self.efinal[k] = h, E + (16 * U * H if hi > lo else 0)
         self.chunks, self.echunks = self.before[:, ::chunk], self.ebefore[:, ::chunk]
-        # The backward keeps 1 - a, rounded to half a step of 1, so there a is off by U (not U a) more, and so are
-        # the states that it recomputes from the chunk states: da_b and eb take the place of da a and ebefore.
-        self.da_b = self.da * self.a + 2 * U
-        self.eb = torch.zeros_like(x)
-        for row, lo, hi, k in self.spans:
-            H, E = init[k].abs(), torch.zeros_like(init[k])
-            for t in range(lo, hi):
-                self.eb[row, t] = E + 16 * U * H
-                a = self.a[row, t]
-                E = a * E + (self.da_b[row, t] + 4 * U * a) * H + self.db * bt[row, t].abs() + m0[row, t]
-                H = a * H + bt[row, t].abs()
-                E = E + 2 * U * H
 
     def grad(self, dy, dfinal=None):
         """{name: (value, bound)}"""
@@ -105,16 +93,15 @@ class Glr:
                 g[row, t], G = dy[row, t] + c, dy[row, t].abs() + C
                 eg[row, t] = E + 16 * U * G
                 c, C = a[row, t] * g[row, t], a[row, t] * G
-                E = a[row, t] * (E + 2 * U * G) + (self.da_b[row, t] + 4 * U * a[row, t]) * G
+                E = a[row, t] * (E + 2 * U * G) + (self.da[row, t] + 4 * U) * C
             dinit[k], edinit[k] = c, E + (16 * U * C if hi > lo else 0)
         ag, ax = g.abs(), x.abs()
         k1 = torch.where(m > 0, q * a * a / m.clamp(min=1e-300), torch.zeros_like(m)) * si * ax
         k2 = q * a
         dqq = torch.where(m > 0, q * a * a / m.clamp(min=1e-300), torch.zeros_like(m)) * si * x * g - k2 * g * self.before
-        e = k1 * (eg + ag * (3 * self.dq + self.ds + 32 * U))
-        e = e + k1 / a.clamp(min=1e-300) * ag * 2 * self.da_b              # a^2: 2 da_b a
-        e = e + k2 * (eg * self.before.abs() + ag * self.eb + ag * self.before.abs() * (self.dq + 16 * U))
-        e = e + q * self.da_b * ag * self.before.abs()
+        e = k1 * (eg + ag * (3 * self.dq + 2 * self.da + self.ds + 32 * U))
+        e = e + k2 * (eg * self.before.abs() + ag * self.ebefore
+                      + ag * self.before.abs() * (self.dq + self.da + 16 * U))
         return {
             "dx": (g * m * si, m * si * (eg + ag * (self.db + 8 * U)) + 2 * M0 * si * ag),
             "di": (g * m * x * si * self.osi, (m * (eg + ag * (self.db + self.ds + 16 * U)) + 2 * M0 * ag) * si * self.osi * ax),
