@@ -307,6 +307,7 @@ template <typename T> struct FwdSmem {
     uint64_t full;                  // the tile's copies have arrived
     int abort;
     Exchange ex;
+    float rate[64];                 // exp(A_log) of the tile's channels
     int4 slot[2];                   // row, step, block of this and the next tile; w: 0 when there is none
 };
 
@@ -375,13 +376,14 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
         const int c = it.blk * 64 + 4 * quad, t0 = it.step * kTile + run * kL, nc = g.D - c;
         const bool live = nc > 0;
-        F4 rate = {f2(0.0f), f2(0.0f)};
-        if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
+        float A_log = 0.0f;
+        if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) A_log = g.A_log[it.blk * 64 + threadIdx.x];
         if constexpr (COPY == 16) {
             if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
         } else {
             copy_wait<0>();
         }
+        if (threadIdx.x < 64) sm.rate[threadIdx.x] = expf(A_log);
         __syncthreads();                            // every warp is done with the tile before
         RunMarks rm{0, 0};
         if constexpr (PACKED) {
@@ -393,22 +395,27 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
                            });
             rm = run_marks(marks, run, lane);
         }
-        const auto ex = [](float v) { return expf(v); };
-        rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
+        const float4 rates = *reinterpret_cast<const float4 *>(&sm.rate[4 * quad]);
+        const F4 rate = values_of(rates);
 
         F4 a[kL], b[kL];
+        const auto gates = [&](auto slow) {
+            constexpr bool SLOW = decltype(slow)::value;
 #pragma unroll
         for (int j = 0; j < kL; ++j) {
             const int row = run * kL + j;
             const F4 r4 = load_gates(&sm.in[0][row][4 * quad]), i4 = load_gates(&sm.in[1][row][4 * quad]), x4 = load4(&sm.in[2][row][4 * quad]);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
-                const Decay2 d = decay2(k.q);
+                const Sigmoids2 k = sigmoids2<SLOW>(r4.p[p], i4.p[p], rate.p[p]);
+                const Decay2 d = decay2<SLOW>(k.q);
                 a[j].p[p] = d.a;
                 b[j].p[p] = mul(mul(scale2(d.e, d.a).m, k.si), x4.p[p]);
             }
         }
+        };
+        if (slow_rates(rates)) gates(std::true_type());
+        else gates(std::false_type());
         if (t0 + kL > g.T) {                        // behind the row's end: the state stays
 #pragma unroll
             for (int j = 0; j < kL; ++j)
@@ -491,6 +498,7 @@ template <typename T> struct BwdSmem {
     Exchange ex;                        // of the scan backwards: its runs are in reverse
     float4 run[kRuns][32];              // maps of the forward scan's runs, later dA_log's sums by warp
     float2 state[32];                   // state that enters the tile
+    float rate[64];                     // exp(A_log) of the tile's channels
     int4 slot[2];
 };
 
@@ -568,8 +576,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         if (threadIdx.x == 0) next = atomicAdd(tl.ticket, 1);
         const int tile = tl.ntiles - 1 - it.step, c = it.blk * 64 + 4 * quad, t0 = tile * kTile + run * kL, nc = g.D - c;
         const bool live = nc > 0;
-        F4 rate = {f2(0.0f), f2(0.0f)};
-        if (live) rate = load4_global<ALIGN>(g.A_log + c, nc);
+        float A_log = 0.0f;
+        if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) A_log = g.A_log[it.blk * 64 + threadIdx.x];
         float2 h0 = make_float2(0.0f, 0.0f);
         if (w == 0) {
             const int cp = it.blk * 64 + 2 * lane;
@@ -601,10 +609,11 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             ir[j] = load_raw4(&sm.in[1][row][4 * quad]);
             xr[j] = load_raw4(&sm.in[2][row][4 * quad]);
         }
+        if (threadIdx.x < 64) sm.rate[threadIdx.x] = expf(A_log);
         __syncthreads();                            // the tile's r, i and x are in registers
         if (w == 0) sm.state[lane] = h0;
-        const auto ex = [](float v) { return expf(v); };
-        rate.p[0] = each(rate.p[0], ex), rate.p[1] = each(rate.p[1], ex);
+        const float4 rates = *reinterpret_cast<const float4 *>(&sm.rate[4 * quad]);
+        const F4 rate = values_of(rates);
         // a sequence's initial state, or the gradient of its final state, of the lane's channels
         const auto of_sequence = [&](const float *p, int s) {
             F4 v = {f2(0.0f), f2(0.0f)};
@@ -618,8 +627,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             F2 A[2], B[2];
 #pragma unroll
             for (int p = 0; p < 2; ++p) A[p] = f2(1.0f), B[p] = f2(0.0f);
-            const auto gates = [&](auto tail_tag) {
-                constexpr bool TAIL = decltype(tail_tag)::value;
+            const auto gates = [&](auto slow, auto tail_tag) {
+                constexpr bool SLOW = decltype(slow)::value, TAIL = decltype(tail_tag)::value;
 #pragma unroll
                 for (int j = 0; j < kL; ++j) {
                     const int row = run * kL + j;
@@ -632,8 +641,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
                     F4 P, Q, O;
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
-                        const Sigmoids2 k = sigmoids2(r4.p[p], i4.p[p], rate.p[p]);
-                        Decay2 d = decay2(k.q);
+                        const Sigmoids2 k = sigmoids2<SLOW>(r4.p[p], i4.p[p], rate.p[p]);
+                        Decay2 d = decay2<SLOW>(k.q);
                         const Scale2 sc = scale2(d.e, d.a);
                         P.p[p] = mul(sc.m, k.si);
                         F2 b = mul(P.p[p], x4.p[p]);
@@ -654,8 +663,10 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
                     sm.kept[2][row][quad] = quad_of(O);
                 }
             };
-            if (tail) gates(std::true_type());
-            else gates(std::false_type());
+            const bool slow = slow_rates(rates);    // (a row's last tile may take the general form)
+            if (__any_sync(0xffffffffu, tail)) gates(std::false_type(), std::true_type());
+            else if (slow) gates(std::true_type(), std::false_type());
+            else gates(std::false_type(), std::false_type());
             Gather<GROUP, PACKED> others;
             others.ask(tl, it, w, lane);
 #pragma unroll

@@ -78,6 +78,8 @@ struct Sigmoids2 {
     F2 q;                       // exp(A_log) sigmoid(r)
     F2 si, osi, osr;            // sigmoid(i), sigmoid(-i), sigmoid(-r)
 };
+// SLOW: rate is at most 1, and q with it.  q is kept above 0 (2^-124).
+template <bool SLOW>
 __device__ __forceinline__ Sigmoids2 sigmoids2(F2 r, F2 i, F2 rate)
 {
     const F2 nlog2e = f2(-1.4426950408889634f), one = f2(1.0f);
@@ -90,44 +92,66 @@ __device__ __forceinline__ Sigmoids2 sigmoids2(F2 r, F2 i, F2 rate)
     g.si = mul(dr, inv);
     g.osr = mul(er, sr);
     g.osi = mul(ei, g.si);
-    g.q = each(mul(rate, sr), [](float v) { return min_nan(v, 87.0f); });
+    g.q = fma(rate, sr, f2(4.70197740e-38f));
+    if (!SLOW) g.q = each(g.q, [](float v) { return min_nan(v, 87.0f); });
     return g;
 }
 
-// 1 - exp(-q), to full relative precision also for small q (1 - a^2 needs it):
-// q = n ln2 + f (two-term ln2, the usual argument reduction), v = 1 - exp(-f) =
-// f u with u a polynomial (degree 5, fitted on |f| <= 0.3467 at Chebyshev
-// nodes, 2.4e-8 of u), s = 2^-n, e = 1 - exp(-q) = s v + (1 - s) and
-// a = exp(-q) = s (1 - v), each to a few roundings of its own size.
+// a = exp(-q) and e = 1 - exp(-q), each to a few roundings of its own size also
+// for small q (1 - a^2 needs e so).
+//
+// SLOW (q <= 1): e = q u, u a polynomial of degree 6 (fitted at Chebyshev nodes
+// on [0, 1], 2.8e-8 of u), a = 1 - e.  Otherwise q = n ln2 + f (the usual
+// argument reduction; the rounded ln2 puts a off by at most 2^-25 q of itself),
+// v = 1 - exp(-f) = f u with u of degree 5 (on |f| <= 0.3467, 2.4e-8), s = 2^-n,
+// e = s v + (1 - s), a = s (1 - v).  9 instructions an element against 4.
 struct Decay2 {
     F2 a, e;
 };
+template <bool SLOW>
 __device__ __forceinline__ Decay2 decay2(F2 q)
 {
+    const F2 minus = f2(-1.0f), one = f2(1.0f);
+    if constexpr (SLOW) {
+        F2 u = fma(q, f2(1.3754070e-4f), f2(-1.3251100e-3f));
+        u = fma(u, q, f2(8.3014267e-3f));
+        u = fma(u, q, f2(-4.1659348e-2f));
+        u = fma(u, q, f2(0.16666605f));
+        u = fma(u, q, f2(-0.5f));
+        u = fma(u, q, one);
+        const F2 e = mul(q, u);
+        return {fma(e, minus, one), e};
+    }
     const F2 k = fma(q, f2(1.4426950408889634f), f2(12582912.0f));       // 1.5 * 2^23: low bits are rint(q log2 e)
     const F2 n = add(k, f2(-12582912.0f));
-    F2 f = fma(n, f2(-0.693359375f), q);                                 // ln2 = 0.693359375 - 2.12194440e-4
-    f = fma(n, f2(2.12194440e-4f), f);
+    const F2 f = fma(n, f2(-0.69314718f), q);
     const F2 s = each(k, [](float v) { return __int_as_float(__float_as_int(v) * -(1 << 23) + (127 << 23)); });
     F2 u = fma(f, f2(-1.39337e-3f), f2(8.36319e-3f));
     u = fma(u, f, f2(-4.166646e-2f));
     u = fma(u, f, f2(0.16666577f));
     u = fma(u, f, f2(-0.5f));
-    u = fma(u, f, f2(1.0f));
-    const F2 v = mul(u, f), minus = f2(-1.0f), one = f2(1.0f);
+    u = fma(u, f, one);
+    const F2 v = mul(u, f);
     return {mul(s, fma(v, minus, one)), fma(s, v, fma(s, minus, one))};
 }
-// m = sqrt(1 - a^2) = sqrt(e (1 + a)) and 1 / m (finite at m = 0: the radicand is kept off 0)
+
+// m = sqrt(1 - a^2) = sqrt(e (1 + a)) and 1 / m (finite, since q is above 0)
 struct Scale2 {
     F2 m, inv_m;
 };
 __device__ __forceinline__ Scale2 scale2(F2 e, F2 a)
 {
-    const F2 w = fma(e, add(a, f2(1.0f)), f2(1.17549435e-38f));
+    const F2 w = fma(e, a, e);
     Scale2 o;
     o.inv_m = each(w, [](float x) { return rsqrt_approx(x); });
     o.m = mul(w, o.inv_m);
     return o;
+}
+
+// Whether every lane's rates are at most 1.
+__device__ __forceinline__ bool slow_rates(float4 r)
+{
+    return __all_sync(0xffffffffu, r.x <= 1.0f && r.y <= 1.0f && r.z <= 1.0f && r.w <= 1.0f);
 }
 
 // Four adjacent channels, as two pairs.  ALIGN is the elements that the

@@ -7,9 +7,10 @@ of float32, relative).  Outputs in bf16 may be off by half a step of bf16 more:
 import torch
 
 U = 2.0 ** -24
-# The kernels take m = sqrt(w + 2^-126) for sqrt(w), w = 1 - a^2, so that 1 / m is finite: off by at most
-# sqrt(2^-126) = 2^-63, which is what is left of it at w = 0.
-M0 = 2.0 ** -63
+# The kernels take q + 2^-124 for q, so that m = sqrt(1 - a^2) is above 0 and 1 / m finite: 1 - a^2 = 1 - exp(-2 q) is
+# off by at most 2^-123, its root by at most 2^-61.5, which is what is left of it at q = 0.  The gradient's q a^2 / m,
+# which goes as sqrt(q / 2) there, is off by at most sqrt(2^-125) = 2^-62.5.
+M0 = 2.0 ** -61
 
 
 def half_step(dtype) -> float:
@@ -102,6 +103,7 @@ class Glr:
         e = k1 * (eg + ag * (3 * self.dq + 2 * self.da + self.ds + 32 * U))
         e = e + k2 * (eg * self.before.abs() + ag * self.ebefore
                       + ag * self.before.abs() * (self.dq + self.da + 16 * U))
+        e = e + 2 * M0 * si * ax * ag + 2.0 ** -123 * ag * self.before.abs()
         return {
             "dx": (g * m * si, m * si * (eg + ag * (self.db + 8 * U)) + 2 * M0 * si * ag),
             "di": (g * m * x * si * self.osi, (m * (eg + ag * (self.db + self.ds + 16 * U)) + 2 * M0 * ag) * si * self.osi * ax),
