@@ -66,42 +66,48 @@ struct Marks {
     int first[TOKENS], last[TOKENS];
 };
 
-// Fills the marks of tokens [t0, t0 + TOKENS), gives sequences without tokens
-// that lie in the tile to `empty`, and checks this CTA's share of cu_seqlens.
-template <int TOKENS, typename Empty>
-__device__ __forceinline__ void mark_sequences(const GlrArgs &g, Marks<TOKENS> &m, int t0, long long cta, long long nctas,
-                                               bool lead, Empty empty)
+// cu_seqlens of a packed batch, in shared memory where it is short.
+constexpr int kNearSeqs = 64;          // four CTAs of float32 just fit an SM
+struct Lengths {
+    int near[kNearSeqs + 1];
+};
+__device__ __forceinline__ void load_lengths(const GlrArgs &g, Lengths &l)
 {
-    const int tid = threadIdx.x, n = blockDim.x;
-    for (int k = tid; k < TOKENS; k += n) m.first[k] = m.last[k] = -1;
-    __syncthreads();
-    // first sequence that may reach into the tile (the array is short, or searched by halves)
-    int lo = 0;
-    if (g.nseq > 1024) {
-        int hi = g.nseq;                                  // smallest s with cu[s + 1] >= t0
-        while (lo < hi) {
+    if (g.nseq <= kNearSeqs)
+        for (int k = threadIdx.x; k <= g.nseq; k += blockDim.x) l.near[k] = g.cu[k];
+}
+
+// Fills the marks of tokens [t0, t0 + TOKENS), a thread a token.  A cu_seqlens
+// that does not ascend gives marks without meaning, but of sequences that exist.
+template <int TOKENS>
+__device__ __forceinline__ void mark_sequences(const GlrArgs &g, const Lengths &l, Marks<TOKENS> &m, int t0)
+{
+    const int *cu = g.nseq <= kNearSeqs ? l.near : g.cu;
+    for (int k = threadIdx.x; k < TOKENS; k += blockDim.x) {
+        const int t = t0 + k;
+        int lo = 0, hi = g.nseq;                          // the last s with cu[s] <= t: it has the token
+        while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (g.cu[mid + 1] >= t0) hi = mid; else lo = mid + 1;
+            if (cu[mid] <= t) lo = mid; else hi = mid;
+        }
+        m.first[k] = cu[lo] == t ? lo : -1;
+        m.last[k] = cu[lo + 1] == t + 1 ? lo : -1;
+    }
+}
+
+// A work item's share of the sequences: checks their lengths, and where there
+// are no tokens hands on to[s] = from[s] (NULL: 0).
+__device__ __forceinline__ void check_sequences(const GlrArgs &g, long long item, long long items, const float *from, float *to)
+{
+    const long long per = (g.nseq + items - 1) / items, end = min((item + 1) * per, (long long)g.nseq);
+    for (long long s = item * per; s < end; ++s) {
+        const int a = g.cu[s], b = g.cu[s + 1];
+        if (a > b || (s == 0 && a != 0) || (s == g.nseq - 1 && b != g.T)) {
+            if (threadIdx.x == 0) set_status(g.status, kDevBadSeqlens);
+        } else if (a == b && to) {
+            for (int c = threadIdx.x; c < g.D; c += blockDim.x) to[s * g.D + c] = from ? from[s * g.D + c] : 0.0f;
         }
     }
-    for (int s = lo + tid; s < g.nseq; s += n) {
-        const int a = g.cu[s], b = g.cu[s + 1];
-        if (a > t0 + TOKENS) break;
-        if (b > a) {
-            if (a >= t0 && a < t0 + TOKENS) m.first[a - t0] = s;
-            if (b > t0 && b <= t0 + TOKENS) m.last[b - 1 - t0] = s;
-        } else if (lead && a >= t0 && (a < t0 + TOKENS || a == g.T)) {
-            // at the end of the row: only the last tile may take it
-            if (a < t0 + TOKENS || t0 + TOKENS >= g.T) empty(s);
-        }
-    }
-    const long long per = (g.nseq + nctas - 1) / nctas;
-    const long long end = min((cta + 1) * per, (long long)g.nseq);
-    for (long long s = cta * per + tid; s < end; s += n) {
-        const int a = g.cu[s], b = g.cu[s + 1];
-        if (a > b || (s == 0 && a != 0) || (s == g.nseq - 1 && b != g.T)) set_status(g.status, kDevBadSeqlens);
-    }
-    __syncthreads();
 }
 
 // ---------------------------------------------------------------- the scan kernels' tiles
@@ -330,7 +336,8 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
 {
     extern __shared__ __align__(128) char smem_raw[];
     FwdSmem<T> &sm = *reinterpret_cast<FwdSmem<T> *>(smem_raw);
-    __shared__ Marks<PACKED ? kTile : 1> marks;
+    __shared__ Marks<PACKED ? kTile : 1> marks2[2];
+    __shared__ std::conditional_t<PACKED, Lengths, int> lengths;
     constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int total = tl.rows * tl.ntiles * tl.nblk;
@@ -357,6 +364,7 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         }
     };
 
+    if constexpr (PACKED) load_lengths(g, lengths);
     if (threadIdx.x == 0) {
         sm.slot[0] = slot_of(tl, atomicAdd(tl.ticket, 1), total);
         sm.abort = 0;
@@ -378,6 +386,11 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         const bool live = nc > 0;
         float A_log = 0.0f;
         if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) A_log = g.A_log[it.blk * 64 + threadIdx.x];
+        auto &marks = marks2[n & 1];
+        if constexpr (PACKED) {
+            mark_sequences(g, lengths, marks, it.step * kTile);
+            check_sequences(g, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, g.init, final_states);
+        }
         if constexpr (COPY == 16) {
             if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
         } else {
@@ -386,15 +399,7 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         if (threadIdx.x < 64) sm.rate[threadIdx.x] = expf(A_log);
         __syncthreads();                            // every warp is done with the tile before
         RunMarks rm{0, 0};
-        if constexpr (PACKED) {
-            mark_sequences(g, marks, it.step * kTile, (long long)it.step * tl.nblk + it.blk,
-                           (long long)tl.ntiles * tl.nblk, true, [&](int s) {
-                               if (!final_states) return;
-                               for (int k = it.blk * 64; k < min((it.blk + 1) * 64, g.D); ++k)
-                                   final_states[(long long)s * g.D + k] = g.init ? g.init[(long long)s * g.D + k] : 0.0f;
-                           });
-            rm = run_marks(marks, run, lane);
-        }
+        if constexpr (PACKED) rm = run_marks(marks, run, lane);
         const float4 rates = *reinterpret_cast<const float4 *>(&sm.rate[4 * quad]);
         const F4 rate = values_of(rates);
 
@@ -527,7 +532,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
 {
     extern __shared__ __align__(128) char smem_raw[];
     BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(smem_raw);
-    __shared__ Marks<PACKED ? kTile : 1> marks;
+    __shared__ Marks<PACKED ? kTile : 1> marks2[2];
+    __shared__ std::conditional_t<PACKED, Lengths, int> lengths;
     constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int back = kRuns - 1 - run;                       // the run in the order of the scan
@@ -557,6 +563,7 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         }
     };
 
+    if constexpr (PACKED) load_lengths(g, lengths);
     if (threadIdx.x == 0) {
         sm.slot[0] = slot_of(tl, atomicAdd(tl.ticket, 1), total);
         sm.abort = 0;
@@ -585,15 +592,10 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (cp < g.D) h0.x = from[0];
             if (cp + 1 < g.D) h0.y = from[1];
         }
-        RunMarks rm{0, 0};
+        auto &marks = marks2[n & 1];
         if constexpr (PACKED) {
-            mark_sequences(g, marks, tile * kTile, (long long)it.step * tl.nblk + it.blk,
-                           (long long)tl.ntiles * tl.nblk, true, [&](int s) {
-                               if (!dinit) return;
-                               for (int k = it.blk * 64; k < min((it.blk + 1) * 64, g.D); ++k)
-                                   dinit[(long long)s * g.D + k] = dfinal ? dfinal[(long long)s * g.D + k] : 0.0f;
-                           });
-            rm = run_marks(marks, run, lane);
+            mark_sequences(g, lengths, marks, tile * kTile);
+            check_sequences(g, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, dfinal, dinit);
         }
         if constexpr (COPY == 16) {
             if (!tc::mbar_wait(&sm.full, n & 1, &sm.abort)) set_status(g.status, kDevTimeout);
@@ -612,6 +614,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         if (threadIdx.x < 64) sm.rate[threadIdx.x] = expf(A_log);
         __syncthreads();                            // the tile's r, i and x are in registers
         if (w == 0) sm.state[lane] = h0;
+        RunMarks rm{0, 0};
+        if constexpr (PACKED) rm = run_marks(marks, run, lane);
         const float4 rates = *reinterpret_cast<const float4 *>(&sm.rate[4 * quad]);
         const F4 rate = values_of(rates);
         // a sequence's initial state, or the gradient of its final state, of the lane's channels

@@ -192,6 +192,20 @@ def test_packed(io, lens, D):
 
 
 @gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("b,T,D,lens", [(2, 200, 72, None), (1, 65, 33, None), (1, 0, 130, [64, 1, 0, 70, 300]),
+                                        (4, 130, 4096, None), (1, 700, 40, [7] * 100)])
+def test_rates_of_at_most_one(io, b, T, D, lens):
+    """Rates of at most 1 have an arithmetic of their own; 4 x 4096 channels fill the SMs, which has shorter groups."""
+    cu = None
+    if lens:
+        cu = [0]
+        for n in lens:
+            cu.append(cu[-1] + n)
+    check(make(b, cu[-1] if cu else T, D, io, cu=cu, hi=0.0, lo=-6.0, seed=D), "cpu" if D < 1000 else "cuda")
+
+
+@gpu
 def test_many_sequences():
     """More sequences than a grid's second dimension holds, most of them empty."""
     n = 70000
