@@ -12,8 +12,8 @@
  * with h_{-1} = initial_states[s, c] (zeros when NULL) and final_states[s, c] =
  * the state after the sequence's last token (the initial state where it has
  * none).  r and i are raw gate logits.  States and all arithmetic are float32;
- * y is rounded once to the io dtype.  Gates below sigmoid(-42.9) = 2^-62 are
- * taken as 2^-62, and q above 87 as 87 (a < 2^-125).
+ * y is rounded once to the io dtype.  Logits below -43 (sigmoid(-43) = 2e-19)
+ * are taken as -43, q above 87 as 87 (a = 2e-38), and 2^-124 is added to q.
  *
  * Layouts:
  *     x, r, i          (batch, seqlen, channels)   io dtype, x_stride (r_stride,
@@ -35,7 +35,8 @@
  * initialisation, may be reused by the next call on the same stream, and must
  * not be shared by calls that can overlap (two captured graphs replayed on two
  * streams need one each).
- * Results do not depend on scheduling: the same call gives the same bits.
+ * Results do not depend on scheduling: the same call on the same device gives
+ * the same bits.
  */
 #ifndef SSD_GLR_H_
 #define SSD_GLR_H_

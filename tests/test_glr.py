@@ -250,6 +250,11 @@ def test_zero_tokens():
         assert torch.equal(final, p["init"])
         got = bwd(p)
         assert torch.equal(got["dinitial_states"], p["dfinal"]) and not got["dA_log"].any()
+    p["cu_t"] = torch.tensor([0, 3, 0], dtype=torch.int32, device="cuda")
+    for call in (fwd, bwd):
+        with pytest.raises(ssd.SsdError) as e:
+            call(p)
+        assert e.value.code == -5
     x = torch.empty((0, 6), dtype=torch.bfloat16, device="cuda")
     assert ssd.ssd_glr_step(x, x, x, torch.zeros(6, device="cuda"), torch.empty((0, 6), device="cuda")).shape == (0, 6)
 
