@@ -523,9 +523,9 @@ template <typename T> struct BwdSmem {
 // before it and H the state that enters the run, so U = U1 - U2 H with U1 and U2
 // known before H is: the gates are evaluated once.  a, U1 and U2 stay in
 // registers over the exchange (96 of them), P, Q and sigmoid(-r) in shared
-// memory, where the tile's inputs were.  (Evaluating the gates again instead
-// cost 83 instructions an element against 58, and 0.37 ms against 0.27 ms on 8 x
-// 2048 x 5120 in bf16.)
+// memory, where the tile's inputs were.  (Evaluating the gates again after the
+// exchange cost 83 instructions an element against 68, and 0.374 ms against
+// 0.341 on 8 x 2048 x 5120 in bf16, with the general form of the gates in both.)
 //
 // part: dA_log's sums of each tile, [row][tile][channels].
 template <typename T, typename G, int COPY, int GROUP, bool PACKED>
