@@ -10,8 +10,8 @@
 // maps through L2, and the thread replays its run from the state that enters it.
 // So x, r, i are read once and y written once, however long the row: the floor
 // is HBM, 104 us for 8 x 2048 x 5120 in bf16 at the measured 6.47 TB/s.  The
-// forward takes 135 us there: 38 instructions an element at 2.4 a clock and SM,
-// 15 of them the gates' (without those it runs at 107 us).
+// forward takes 135 us there: 33 instructions an element at 2.4 a clock and SM,
+// 14 of them the gates' (with those left out it runs at 107 us).
 //
 // Tiles of one row wait for earlier tiles' maps.  Work is handed out by a
 // ticket, earlier tiles first, and a tile publishes its own map before it
@@ -146,7 +146,7 @@ struct Gather {
     static constexpr int N = GROUP / kWarps;
     const float4 *maps;
     const float2 *before;
-    uint4 m[N];
+    uint4 m[N > 0 ? N : 1];
     uint2 s;
     int cnt;
     bool state;
