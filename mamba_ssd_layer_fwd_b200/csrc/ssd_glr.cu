@@ -701,7 +701,17 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             }
 #pragma unroll
             for (int p = 0; p < 2; ++p) sm.ex.run[back][2 * quad + p] = pack_map(A[p], B[p]);
-            if (threadIdx.x == 0) sm.slot[(n + 1) & 1] = slot_of(tl, next, total);
+            if (threadIdx.x == 0) {
+                const int4 s = slot_of(tl, next, total);
+                sm.slot[(n + 1) & 1] = s;
+                if (COPY == 16 && s.w) {            // there is no room for it yet, but in L2
+                    const int c0 = s.z * 64, tok = s.x * g.T + (tl.ntiles - 1 - s.y) * kTile;
+                    tc::tma_prefetch_l2_2d(&maps.r, c0, tok);
+                    tc::tma_prefetch_l2_2d(&maps.i, c0, tok);
+                    tc::tma_prefetch_l2_2d(&maps.x, c0, tok);
+                    tc::tma_prefetch_l2_2d(&maps.dy, c0, tok);
+                }
+            }
             __syncthreads();
             const Map4 before = runs_before<PACKED>(sm.ex.run, back, quad);
             if (back == kRuns - 1) post_map<GROUP, PACKED>(tl, it, before, sm.ex, quad);
@@ -814,14 +824,17 @@ __global__ void __launch_bounds__(kThreads) glr_no_tokens_kernel(GlrArgs g, cons
 template <int ALIGN, typename T>
 __device__ __forceinline__ typename Raw4<T>::type load_raw4_global(const T *p, int n)
 {
-    if constexpr (ALIGN == 4) return load_raw4(p);
-    union {
-        T v[4];
-        typename Raw4<T>::type q;
-    } u;
+    if constexpr (ALIGN == 4) {
+        return load_raw4(p);
+    } else {
+        union {
+            T v[4];
+            typename Raw4<T>::type q;
+        } u;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) u.v[k] = k < n ? p[k] : from_f32<T>(0.0f);
-    return u.q;
+        for (int k = 0; k < 4; ++k) u.v[k] = k < n ? p[k] : from_f32<T>(0.0f);
+        return u.q;
+    }
 }
 
 // One token of every row, four channels a thread.  A few thousand threads at
