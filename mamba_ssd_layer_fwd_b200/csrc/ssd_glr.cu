@@ -115,6 +115,8 @@ __device__ __forceinline__ void check_sequences(const GlrArgs &g, long long item
 }
 
 // ---------------------------------------------------------------- the scan kernels' tiles
+constexpr int kShortGroup = 4, kLongGroup = 16;     // tiles of a group
+
 // A CTA of kWarps warps walks tiles of kTile tokens by 64 channels.  A lane has
 // four adjacent channels of a run of kL tokens, half a warp one run.
 constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kThreads = 32 * kWarps;
@@ -631,6 +633,9 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         const bool tail = t0 + kL > g.T;
 
         F4 a[kL], u1[kL], u2[kL];
+        Gather<GROUP, PACKED> others;
+        constexpr bool EARLY = GROUP == kShortGroup;    // few registers, and mostly there already
+        if (EARLY) others.ask(tl, it, w, lane);
         {
             F2 A[2], B[2];
 #pragma unroll
@@ -675,8 +680,7 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (__any_sync(0xffffffffu, tail)) gates(std::false_type(), std::true_type());
             else if (slow) gates(std::true_type(), std::false_type());
             else gates(std::false_type(), std::false_type());
-            Gather<GROUP, PACKED> others;
-            others.ask(tl, it, w, lane);
+            if (!EARLY) others.ask(tl, it, w, lane);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
                 sm.run[run][2 * quad + p] = pack_map(A[p], B[p]);
@@ -923,7 +927,6 @@ int sm_count()
 // maps (8 x 2048 x 5120 bf16: 0.149 ms against 0.161 with 16); with fewer
 // blocks many tiles of a row are in work at once and what counts is that the
 // chain of states is short (16384 x 2048 bf16: 0.101 ms against 0.118).
-constexpr int kShortGroup = 4, kLongGroup = 16;
 int group_of(const Tiling &t) { return t.rows * t.nblk >= sm_count() ? kShortGroup : kLongGroup; }
 
 // Workspace of one scan: status word, ticket counter, and the maps and states

@@ -130,12 +130,56 @@ __device__ __forceinline__ float cta_sum(float v, float *slots)
     return team_sum(v, 32);
 }
 
+// float32 parameters of a thread's columns (zeros where there are none)
+template <int V, int NV>
+__device__ __forceinline__ void load_params(const float *p, int P, int t, int n, F2 (&f)[V * NV / 2])
+{
+    float v[V * NV];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+        const int c = (t + k * n) * V;
+        const bool in = p && c < P;
+#pragma unroll
+        for (int q = 0; q < V; q += 4) {
+            if constexpr (V == 1) {
+                v[k] = in ? p[c] : 0.0f;
+            } else {
+                const float4 o = in ? *reinterpret_cast<const float4 *>(p + c + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                v[k * V + q] = o.x, v[k * V + q + 1] = o.y, v[k * V + q + 2] = o.z, v[k * V + q + 3] = o.w;
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < V * NV / 2; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
+}
+
+// Parameters of the k-th piece of a thread's columns: kept in registers, or read
+// where they are used.
+template <int H, int HP> struct KeptWeights {
+    const F2 (&all)[H];
+    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
+    {
+#pragma unroll
+        for (int j = 0; j < HP; ++j) w[j] = all[k * HP + j];
+    }
+};
+template <int V, int NV, int HP> struct ReadWeights {
+    const float *p;
+    int P, t, n;
+    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
+    {
+        if constexpr (V == 1) load_params<1, NV>(p, P, t, n, w);
+        else load_params<V, 1>(p, P, t + k * n, n, w);
+    }
+};
+
 // ---------------------------------------------------------------- forward
 
 // A thread's part of one row: vectors t, t + n, ... of the group that starts at
 // channel c0.
 template <typename T, int V, int NV, Mode M> struct FwdRow {
     static constexpr int H = V * NV / 2;
+    static constexpr int NP = V == 1 ? 1 : NV, HP = H / NP;     // pieces (vectors) and their pairs
     Raw<T, V, NV> x;
     Raw<T, V, M == kPlain ? 2 : NV> z;
     F2 u[H];
@@ -220,20 +264,33 @@ template <typename T, int V, int NV, Mode M> struct FwdRow {
         return total(s);
     }
 
+    // weights(k, w), biases(k, b): of the k-th piece of the thread's columns
+    template <typename W, typename B>
     __device__ __forceinline__ void write(const NormArgs &a, long long row, int g, int t, int n, bool live, float mu,
-                                          float rs, const F2 (&w)[H], const F2 (&b)[H], T *y, float *mean, float *rstd)
+                                          float rs, const W &weights, const B &biases, T *y, float *mean, float *rstd)
     {
         if (!live) return;
         if (t == 0) {
             if (mean) mean[row * a.G + g] = mu;
             if (rstd) rstd[row * a.G + g] = rs;
         }
+        T *to = y + row * a.D + (long long)g * a.P;
 #pragma unroll
-        for (int i = 0; i < H; ++i) u[i] = fma(mul(u[i], f2(rs)), w[i], b[i]);
+        for (int k = 0; k < NP; ++k) {
+            F2 w[HP], b[HP];
+            weights(k, w);
+            biases(k, b);
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-            const int c = (t + k * n) * V;
-            if (c < a.P) store_vector<T, V>(y + row * a.D + (long long)g * a.P + c, k, u);
+            for (int j = 0; j < HP; ++j) u[k * HP + j] = fma(mul(u[k * HP + j], f2(rs)), w[j], b[j]);
+            if constexpr (V > 1) {
+                const int c = (t + k * n) * V;
+                if (c < a.P) store_vector<T, V>(to + c, k, u);
+            }
+        }
+        if constexpr (V == 1) {
+#pragma unroll
+            for (int k = 0; k < NV; ++k)
+                if (t + k * n < a.P) store_vector<T, V>(to + t + k * n, k, u);
         }
     }
 };
@@ -243,29 +300,6 @@ __device__ __forceinline__ float mean_of(float s, int P, float inv)
 {
     const float mu = s * inv;
     return fmaf(fmaf(-mu, (float)P, s), inv, mu);
-}
-
-// float32 parameters of a thread's columns (zeros where there are none)
-template <int V, int NV>
-__device__ __forceinline__ void load_params(const float *p, int P, int t, int n, F2 (&f)[V * NV / 2])
-{
-    float v[V * NV];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-        const int c = (t + k * n) * V;
-        const bool in = p && c < P;
-#pragma unroll
-        for (int q = 0; q < V; q += 4) {
-            if constexpr (V == 1) {
-                v[k] = in ? p[c] : 0.0f;
-            } else {
-                const float4 o = in ? *reinterpret_cast<const float4 *>(p + c + q) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                v[k * V + q] = o.x, v[k * V + q + 1] = o.y, v[k * V + q + 2] = o.z, v[k * V + q + 3] = o.w;
-            }
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < V * NV / 2; ++i) f[i] = f2(v[2 * i], v[2 * i + 1]);
 }
 
 // A lane's own ring in shared memory for kDepth rows of N pieces of 16 bytes and
@@ -299,9 +333,10 @@ norm_fwd_team_kernel(NormArgs a, int lanes, int ncols, T *__restrict__ y, T *__r
     const long long first = (long long)(blockIdx.x / ncols) * W + (threadIdx.x >> 5), step = (long long)(gridDim.x / ncols) * W;
     const bool live = g < a.G;
     const float inv = 1.0f / a.P;
-    F2 w[H], b[H];
-    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, w);
-    load_params<V, NV>(live && a.b ? a.b + c0 : nullptr, a.P, t, lanes, b);
+    F2 wk[H], bk[H];
+    load_params<V, NV>(live ? a.w + c0 : nullptr, a.P, t, lanes, wk);
+    load_params<V, NV>(live && a.b ? a.b + c0 : nullptr, a.P, t, lanes, bk);
+    const KeptWeights<H, FwdRow<T, V, NV, M>::HP> w{wk}, b{bk};
     for (long long row = first; row < a.rows; row += R * step) {
         FwdRow<T, V, NV, M> r[R];
         float s[R], mu[R];
@@ -325,7 +360,6 @@ __global__ void __launch_bounds__(MAXT, 1)
 norm_fwd_cta_kernel(NormArgs a, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean, float *__restrict__ rstd)
 {
     __shared__ float slots[2][32];
-    constexpr int H = V * NV / 2;
     const unsigned unit = blockIdx.x, row = unit / a.G;
     const int g = unit - row * a.G, t = threadIdx.x, n = blockDim.x, c0 = g * a.P;
     const float inv = 1.0f / a.P;
@@ -333,19 +367,17 @@ norm_fwd_cta_kernel(NormArgs a, T *__restrict__ y, T *__restrict__ sum, float *_
     r.load(a, row, c0, t, n, true);
     const float mu = mean_of(cta_sum(r.input(a, row, c0, t, n, true, sum), slots[0]), a.P, inv);
     const float rs = rsqrtf(fmaf(cta_sum(r.centre(a, mu, t, n), slots[1]), inv, a.eps));
-    F2 w[H], b[H];                                  // from L1 by now; registers make room for more CTAs
-    load_params<V, NV>(a.w + c0, a.P, t, n, w);
-    load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
-    r.write(a, row, g, t, n, true, mu, rs, w, b, y, mean, rstd);
+    typedef ReadWeights<V, NV, FwdRow<T, V, NV, M>::HP> Read;
+    r.write(a, row, g, t, n, true, mu, rs, Read{a.w + c0, a.P, t, n}, Read{a.b ? a.b + c0 : nullptr, a.P, t, n}, y, mean, rstd);
 }
 
 // The same for many rows that are aligned to 16 bytes: a CTA keeps one group's
 // columns and walks rows that thread 0 copies `nst` ahead into shared memory,
 // so that HBM reads go on through the two reductions of a row.
-constexpr int kMaxStages = 6;
+constexpr int kMaxStages = 6, kRingCtas = 4;
 
 template <typename T, int V, int NV, Mode M>
-__global__ void __launch_bounds__(384, 2)
+__global__ void __launch_bounds__(384, kRingCtas)
 norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum, float *__restrict__ mean,
                      float *__restrict__ rstd)
 {
@@ -353,7 +385,6 @@ norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum
     __shared__ float slots[2][32];
     __shared__ uint64_t full[kMaxStages];
     __shared__ int abort_wait;
-    constexpr int H = V * NV / 2;
     const int t = threadIdx.x, n = blockDim.x;
     const int g = blockIdx.x % a.G, split_ = blockIdx.x / a.G, nsplit = gridDim.x / a.G, c0 = g * a.P;
     const float inv = 1.0f / a.P;
@@ -373,6 +404,8 @@ norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum
         tc::mbar_fence_init();
         for (int q = 0; q < min(nst, count); ++q) send(q, q);
     }
+    typedef ReadWeights<V, NV, Row::HP> Read;       // from L1: registers make room for more CTAs
+    const Read w{a.w + c0, a.P, t, n}, b{a.b ? a.b + c0 : nullptr, a.P, t, n};
     __syncthreads();
     int stage = 0, parity = 0;
     for (int q = 0; q < count; ++q) {
@@ -387,9 +420,6 @@ norm_fwd_ring_kernel(NormArgs a, int nst, T *__restrict__ y, T *__restrict__ sum
         const float mu = mean_of(cta_sum(r.input(a, row, c0, t, n, true, sum), slots[0]), a.P, inv);
         if (t == 0 && q + nst < count) send(q + nst, stage);    // a barrier ago the row was in registers
         const float rs = rsqrtf(fmaf(cta_sum(r.centre(a, mu, t, n), slots[1]), inv, a.eps));
-        F2 w[H], b[H];
-        load_params<V, NV>(a.w + c0, a.P, t, n, w);
-        load_params<V, NV>(a.b ? a.b + c0 : nullptr, a.P, t, n, b);
         r.write(a, row, g, t, n, true, mu, rs, w, b, y, mean, rstd);
         if (++stage == nst) stage = 0, parity ^= 1;
     }
@@ -501,26 +531,6 @@ template <typename T, typename G, int V, int NV, bool GATE> struct BwdRow {
                 if constexpr (GATE) store_vector<G, V>(dz + c, k, oz);
             }
         }
-    }
-};
-
-// Weights of the k-th piece of a thread's columns: kept in registers, or read
-// where they are used.
-template <int H, int HP> struct KeptWeights {
-    const F2 (&all)[H];
-    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
-    {
-#pragma unroll
-        for (int j = 0; j < HP; ++j) w[j] = all[k * HP + j];
-    }
-};
-template <int V, int NV, int HP> struct ReadWeights {
-    const float *p;
-    int P, t, n;
-    __device__ __forceinline__ void operator()(int k, F2 (&w)[HP]) const
-    {
-        if constexpr (V == 1) load_params<1, NV>(p, P, t, n, w);
-        else load_params<V, 1>(p, P, t + k * n, n, w);
     }
 };
 
@@ -904,7 +914,7 @@ void fwd_cta(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStre
 template <typename T, int V, int NV, Mode M>
 bool fwd_ring(const NormArgs &a, T *y, T *sum, float *mean, float *rstd, cudaStream_t st)
 {
-    const int t = threads_of((a.P + V - 1) / V, NV), per_sm = std::min(6, 65536 / (80 * t));
+    const int t = threads_of((a.P + V - 1) / V, NV), per_sm = std::min(6, kRingCtas * 384 / t);
     const int n = sm_count() * per_sm / a.G;
     if (n < 1 || a.rows < 2 * n) return false;      // a row or two a CTA: nothing to copy ahead
     const auto kernel = norm_fwd_ring_kernel<T, V, NV, M>;
