@@ -82,9 +82,8 @@ __device__ __forceinline__ void load_lengths(const GlrArgs &g, Lengths &l)
 // Fills the marks of tokens [t0, t0 + TOKENS), a thread a token.  A cu_seqlens
 // that does not ascend gives marks without meaning, but of sequences that exist.
 template <int TOKENS>
-__device__ __forceinline__ void mark_sequences(const GlrArgs &g, const Lengths &l, Marks<TOKENS> &m, int t0)
+__device__ __forceinline__ void mark_sequences(const GlrArgs &g, const int *cu, Marks<TOKENS> &m, int t0)
 {
-    const int *cu = g.nseq <= kNearSeqs ? l.near : g.cu;
     for (int k = threadIdx.x; k < TOKENS; k += blockDim.x) {
         const int t = t0 + k;
         int lo = 0, hi = g.nseq;                          // the last s with cu[s] <= t: it has the token
@@ -120,7 +119,7 @@ constexpr int kShortGroup = 4, kLongGroup = 16;     // tiles of a group
 // A CTA of kWarps warps walks tiles of kTile tokens by 64 channels.  A lane has
 // four adjacent channels of a run of kL tokens, half a warp one run.
 constexpr int kL = 8, kWarps = 4, kRuns = 2 * kWarps, kTile = kL * kRuns, kThreads = 32 * kWarps;
-static_assert(kWarps * 16 <= kRuns * 32, "room for the sums");
+static_assert(kWarps * 16 <= (kRuns - 1) * 32, "room for the sums");
 static_assert(kTile == SSD_GLR_CHUNK, "a tile starts at a chunk state");
 
 __device__ __forceinline__ float4 pack_map(F2 A, F2 B)
@@ -211,7 +210,7 @@ struct Map4 {
 
 // Composition of the maps of the tile's runs before `run`, of a lane's channels.
 template <bool PACKED>
-__device__ __forceinline__ Map4 runs_before(const float4 (&maps)[kRuns][32], int run, int quad)
+__device__ __forceinline__ Map4 runs_before(const float4 (*maps)[32], int run, int quad)
 {
     Map4 m = {{f2(1.0f), f2(1.0f)}, {f2(0.0f), f2(0.0f)}};
 #pragma unroll
@@ -394,7 +393,7 @@ glr_fwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, T *
         if (threadIdx.x < 64 && it.blk * 64 + threadIdx.x < g.D) A_log = g.A_log[it.blk * 64 + threadIdx.x];
         auto &marks = marks2[n & 1];
         if constexpr (PACKED) {
-            mark_sequences(g, lengths, marks, it.step * kTile);
+            mark_sequences(g, g.nseq <= kNearSeqs ? lengths.near : g.cu, marks, it.step * kTile);
             check_sequences(g, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, g.init, final_states);
         }
         if constexpr (COPY == 16) {
@@ -507,7 +506,7 @@ template <typename T> struct BwdSmem {
     uint64_t full;
     int abort;
     Exchange ex;                        // of the scan backwards: its runs are in reverse
-    float4 run[kRuns][32];              // maps of the forward scan's runs, later dA_log's sums by warp
+    float4 run[kRuns - 1][32];          // maps of the forward scan's runs but the last, later dA_log's sums by warp
     float2 state[32];                   // state that enters the tile
     float rate[64];                     // exp(A_log) of the tile's channels
     int4 slot[2];
@@ -538,8 +537,7 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
 {
     extern __shared__ __align__(128) char smem_raw[];
     BwdSmem<T> &sm = *reinterpret_cast<BwdSmem<T> *>(smem_raw);
-    __shared__ Marks<PACKED ? kTile : 1> marks2[2];
-    __shared__ std::conditional_t<PACKED, Lengths, int> lengths;
+    __shared__ Marks<PACKED ? kTile : 1> marks;
     constexpr int ALIGN = COPY == 16 ? 4 : COPY / (int)sizeof(T);
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, quad = lane & 15, half = lane >> 4, run = 2 * w + half;
     const int back = kRuns - 1 - run;                       // the run in the order of the scan
@@ -569,7 +567,6 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         }
     };
 
-    if constexpr (PACKED) load_lengths(g, lengths);
     if (threadIdx.x == 0) {
         sm.slot[0] = slot_of(tl, atomicAdd(tl.ticket, 1), total);
         sm.abort = 0;
@@ -598,9 +595,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (cp < g.D) h0.x = from[0];
             if (cp + 1 < g.D) h0.y = from[1];
         }
-        auto &marks = marks2[n & 1];
         if constexpr (PACKED) {
-            mark_sequences(g, lengths, marks, tile * kTile);
+            mark_sequences(g, g.cu, marks, tile * kTile);
             check_sequences(g, (long long)it.step * tl.nblk + it.blk, (long long)tl.ntiles * tl.nblk, dfinal, dinit);
         }
         if constexpr (COPY == 16) {
@@ -683,7 +679,7 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
             if (!EARLY) others.ask(tl, it, w, lane);
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                sm.run[run][2 * quad + p] = pack_map(A[p], B[p]);
+                if (run < kRuns - 1) sm.run[run][2 * quad + p] = pack_map(A[p], B[p]);
                 if (PACKED) A[p] = f2(1.0f);
                 B[p] = f2(0.0f);
             }
@@ -788,6 +784,8 @@ glr_bwd_kernel(const __grid_constant__ InputMaps maps, GlrArgs g, Tiling tl, con
         }
     }
 }
+
+static_assert(3 * (sizeof(BwdSmem<float>) + sizeof(Marks<kTile>) + 1024) <= 228 * 1024, "three CTAs an SM");
 
 // dA_log: the sum of the tiles' parts.  A CTA has 32 channels; eight warps take
 // every eighth tile and their sums are added in order.
