@@ -206,6 +206,40 @@ def test_rates_of_at_most_one(io, b, T, D, lens):
 
 
 @gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_thirds_of_one_projection_and_offsets_beyond_32_bits(io):
+    """x, r and i as column ranges: of one tensor, and of one whose last rows lie 2^31 elements behind its first."""
+    D = 72
+    p = make(2, 133, D, io, seed=21)
+    proj = torch.cat([p["x"], p["r"], p["i"]], -1)
+    p["x"], p["r"], p["i"] = proj.split(D, -1)
+    check(p)
+    T, stride = 20000, 110000
+    p = make(1, T, D, io, seed=22, hi=0.0)
+    big = torch.empty(T * stride, dtype=IO[io], device="cuda").view(1, T, stride)
+    assert (T - 1) * stride > 2 ** 31
+    big[..., 8:8 + 3 * D] = torch.cat([p["x"], p["r"], p["i"]], -1)
+    want = fwd(p)
+    grads = bwd(p, chunk_states=want[2])
+    p["x"], p["r"], p["i"] = big[..., 8:8 + 3 * D].split(D, -1)
+    assert all(torch.equal(a, b) for a, b in zip(fwd(p), want))
+    got = bwd(p, chunk_states=want[2])
+    assert all(torch.equal(got[k], grads[k]) for k in grads)
+
+
+@gpu
+def test_a_given_stream_and_a_call_after_it():
+    p = make(2, 500, 64, "bf16", seed=23)
+    want = fwd(p)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = ssd.ssd_glr_fwd(p["x"], p["r"], p["i"], p["A_log"], initial_states=p["init"], return_final_states=True,
+                          return_chunk_states=True, stream=s)
+    s.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@gpu
 def test_many_sequences():
     """More sequences than a grid's second dimension holds, most of them empty."""
     n = 70000

@@ -176,6 +176,38 @@ def test_many_rows(io):
 
 
 @gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("kind", ["plain", "residual", "gate"])
+@pytest.mark.parametrize("shape,groups", [((3001, 1544), 1), ((2403, 2560), 1), ((1501, 5120), 1), ((700, 8192), 2),
+                                          ((1600, 6152), 1)])
+def test_many_long_rows(io, kind, shape, groups):
+    """Rows enough that a CTA walks several of them."""
+    check(make(shape, io, groups, kind, seed=shape[0]), device="cuda")
+
+
+@gpu
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,D,groups", [(2500, 1280, 1), (900, 640, 10), (2000, 512, 1)])
+def test_columns_of_a_wider_tensor(io, rows, D, groups):
+    """x and z as aligned column ranges of one tensor, forward and backward."""
+    p = make((rows, D), io, groups, "gate", seed=D)
+    wide = torch.cat([p["x"], p["dy"], p["z"]], -1)
+    p["x"], p["z"] = wide[:, :D], wide[:, 2 * D:]
+    check(p, device="cuda")
+
+
+@gpu
+def test_offsets_beyond_32_bits():
+    rows, D, stride = 20000, 64, 110000
+    assert (rows - 1) * stride > 2 ** 31
+    p = make((rows, D), "bf16", 2, "gate", seed=31)
+    big = torch.empty(rows * stride, dtype=torch.bfloat16, device="cuda").view(rows, stride)
+    big[:, 16:16 + D], big[:, 512:512 + D] = p["x"], p["z"]
+    p["x"], p["z"] = big[:, 16:16 + D], big[:, 512:512 + D]
+    check(p, device="cuda")
+
+
+@gpu
 def test_a_row_far_from_zero_and_a_row_of_one_value():
     p = make((6, 1000), "f32", seed=3)
     p["x"][0] += 1000.0                       # mean far above the spread
