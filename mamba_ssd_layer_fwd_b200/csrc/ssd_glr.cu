@@ -10,7 +10,7 @@
 // maps through L2, and the thread replays its run from the state that enters it.
 // So x, r, i are read once and y written once, however long the row: the floor
 // is HBM, 104 us for 8 x 2048 x 5120 in bf16 at the measured 6.47 TB/s.  The
-// forward takes 135 us there: 33 instructions an element at 2.4 a clock and SM,
+// forward takes 136 us there: 32 instructions an element at 2.3 a clock and SM,
 // 14 of them the gates' (with those left out it runs at 107 us).
 //
 // Tiles of one row wait for earlier tiles' maps.  Work is handed out by a
